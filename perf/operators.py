@@ -408,8 +408,8 @@ def _run_append(s):
 def _run_commit(s):
     if own:
         import latent_attention_decode_absorbed_b200 as mla
-        mla.mla_cache_commit(s["kv_lens"], s["row_start"], s["B"], s["counts"], s["nodes"], s["table"],
-                             s["table"].shape[1], PAGE, s["pool"], s["scale"], _codes(mla)[s["cache_kind"]],
+        mla.mla_cache_commit(s["kv_lens"], s["row_start"], s["B"], s["B"] * s["n"], s["counts"], s["nodes"],
+                             s["table"], s["table"].shape[1], PAGE, s["pool"], s["scale"], _codes(mla)[s["cache_kind"]],
                              s["num_pages"], s["seq_lens"])
         return {**_pool_out(s), "seq_lens": s["seq_lens"]}
     start = s["row_start"].long()
