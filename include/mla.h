@@ -31,6 +31,14 @@
  *   (mla_combine_shards: the same merge over the per-GPU results of sequences
  *    whose cached rows are sharded across GPUs)
  *   mla_out_uv        o_lat         -> out = W_UV o_lat                 (128 per head)
+ * A step that checks drafted tokens (a tree of guesses per sequence, several
+ * rows of ragged number each) plans and runs on the GPU without its host
+ * knowing any length:
+ *   mla_step_plan           lengths, row counts, trees -> pages, block table, slots, positions, masks
+ *   mla_cache_append_slots  new kv_a rows -> cache rows at the planned slots
+ *   mla_decode_tree         q_abs, cache, masks -> o_lat, lse (attention and merge)
+ *   mla_cache_commit        the accepted path's rows -> the front of the drafted rows, new lengths
+ * with mla_absorb_q before and mla_out_uv after the attention.
  * and the projections on either side of that core:
  *   mla_kv_proj_append  hidden states h -> kv_a = W_kv,a h -> cache rows (one kernel)
  *   mla_out_proj        out (all heads) -> u = W_O [o_1; ...; o_H]
@@ -91,6 +99,7 @@ typedef enum {
 #define MLA_DEVERR_PAGE     0x1  /* block-table entry < 0 or >= num_pages: row skipped */
 #define MLA_DEVERR_POSITION 0x2  /* append position/sequence outside the table: row skipped */
 #define MLA_DEVERR_TIMEOUT  0x4  /* a bounded device wait gave up: results invalid */
+#define MLA_DEVERR_CAPACITY 0x8  /* mla_step_plan: the step does not fit (pages, rows, table, mask): nothing planned */
 
 /* Short static string for a status code; never NULL. */
 const char* mla_status_string(int status);
@@ -281,6 +290,159 @@ mla_status mla_decode_fwd_q8(const void* q8, const float* q_scale, const void* c
                              const int32_t* seq_lens, int batch, int q_len, int n_heads, int num_splits,
                              int split_tokens, float softmax_scale, float* o_part, float* lse_part,
                              int32_t* err_word, cudaStream_t stream);
+
+/*
+ * mla_step_plan
+ * The bookkeeping of one step, on the GPU: which rows and pages the step's new
+ * tokens take.  Not a step of the method itself; the paged cache that it lays
+ * out is the one of "KV Compression - DeepSeek-V3", "How it works".
+ * Sequence b has L_b = seq_lens[b] cached rows, n_b = new_counts[b] new rows and
+ * held_in[b] pages (the first entries of its block-table row).  With
+ * need_b = ceil((L_b + n_b) / page_size):
+ *   pages    where held_in[b] > need_b the surplus returns to the free list (its
+ *            table entries become -1), in sequence and table order behind the
+ *            list's end; then, in the same order, each missing page is the
+ *            list's last, and held_out[b] = need_b.  So a finished sequence is
+ *            released by seq_lens[b] = new_counts[b] = 0.
+ *   row_start[0..batch]  offsets of the sequences' new rows, row_start[batch] = all of them
+ *   kv_lens[b] = L_b + n_b
+ *   and for new row r = row_start[b] + i (cached row L_b + i of its sequence)
+ *   seq_ids[r] = b
+ *   slots[r] = table[b, (L_b + i) / page_size] * page_size + (L_b + i) % page_size
+ *   positions[r] = L_b + i, or with parents L_b + (number of ancestors of i)
+ *   tree_mask[r, w] bit k: node 64 w + k is i or an ancestor of i (without
+ *            parents: 64 w + k <= i)
+ *   rows behind the last sequence: seq_ids and slots -1, positions and masks 0
+ *   seq_lens, new_counts  device int32 [batch]
+ *   parents     device int32 [max_rows] or NULL (no trees: the new rows follow one
+ *               another): the parent of each new row within its own sequence's rows,
+ *               negative for a root; a parent comes before its children (another
+ *               one is flagged MLA_DEVERR_POSITION and taken as no parent)
+ *   held_in, held_out     device int32 [batch]; may be one buffer
+ *   free_pages  device int32 [num_pages], its first *free_count_in entries the free list
+ *   free_count_in, free_count_out  device int32 [1]; may be one buffer
+ *   block_table device int32 [batch, max_pages_per_seq], updated
+ *   row_start   device int32 [batch + 1];  kv_lens device int32 [batch]
+ *   seq_ids     device int32 [max_rows] or NULL;  positions, slots device int32 [max_rows]
+ *   tree_mask   device uint64 [max_rows, mask_words] or NULL
+ *   err_word    device int32 or NULL.  MLA_DEVERR_CAPACITY: too few free pages, more
+ *               than max_rows new rows, a sequence beyond its table row, or a tree
+ *               beyond 64 mask_words nodes.  MLA_DEVERR_POSITION: a negative length,
+ *               count or held number, or a free count that cannot be.  In both cases
+ *               nothing is planned: pages, table, held and free count stay as they
+ *               were, row_start is all 0, kv_lens = seq_lens and every slot -1, so
+ *               that the calls that follow do no work.  MLA_DEVERR_PAGE: a row's page
+ *               is outside the pool; its slot is -1.
+ * Except held and free_count, outputs must not overlap inputs.  Host limits:
+ * num_pages * page_size, max_pages_per_seq * page_size and batch *
+ * max_pages_per_seq below 2^31.  One launch up to 4096 rows, two above.
+ */
+mla_status mla_step_plan(const int32_t* seq_lens, const int32_t* new_counts, const int32_t* parents, int batch,
+                         int max_rows, int mask_words, const int32_t* held_in, int32_t* held_out, int32_t* free_pages,
+                         const int32_t* free_count_in, int32_t* free_count_out, int32_t* block_table,
+                         int max_pages_per_seq, int page_size, int num_pages, int32_t* row_start, int32_t* kv_lens,
+                         int32_t* seq_ids, int32_t* positions, int32_t* slots, uint64_t* tree_mask,
+                         int32_t* err_word, cudaStream_t stream);
+
+/*
+ * mla_cache_append_slots
+ * mla_cache_append's rows (RMSNorm, RoPE, cast or quantise: the same bits) at
+ * given slots: row n is stored at slots[n] of the pool and its key rotated to
+ * positions[n].  In a drafted tree the two are independent, since siblings
+ * share a position but not a slot.
+ *   slots     device int32 [n_new], each in [0, num_pages * 64), or -1: the row is
+ *             skipped (padding behind a step's last row); others are flagged
+ *             MLA_DEVERR_PAGE and skipped
+ *   positions device int32 [n_new], each in [0, rope_max_pos), else flagged
+ *             MLA_DEVERR_POSITION and skipped
+ *   the other arguments as for mla_cache_append.  Rows with one slot race.
+ */
+mla_status mla_cache_append_slots(const void* kv_a, mla_dtype kv_dtype, int n_new, const int32_t* slots,
+                                  const int32_t* positions, const float* norm_gain, float eps, const float* rope_cos,
+                                  const float* rope_sin, int rope_max_pos, void* cache, float* cache_scale,
+                                  mla_dtype cache_dtype, int num_pages, int32_t* err_word, cudaStream_t stream);
+
+/*
+ * mla_decode_tree_workspace_bytes (host function, no GPU needed)
+ * Bytes of caller workspace mla_decode_tree needs for a call of max_rows rows
+ * with this cache: for bf16 a fixed 50 MB of fp32 partials, for e4m3 also
+ * 1156 bytes per (row, head) for the two-term query, for fp32 32.8 KB per
+ * (row, head).  0 for non-positive sizes or an unknown dtype.
+ */
+size_t mla_decode_tree_workspace_bytes(mla_dtype cache_dtype, int max_rows, int n_heads);
+
+/*
+ * mla_decode_tree
+ * Attention and merge for a ragged number of drafted tokens per sequence
+ * ("DeepSeek-V2: MLA Explained", "MLA Full Formulas" part 3 with the absorption
+ * of "Optimization Note"; the visibility is a tree's instead of a chain's).
+ * Sequence b has n_b = row_start[b+1] - row_start[b] query rows and L_b =
+ * kv_lens[b] cached rows, the last n_b of them its drafted rows.  Query row r =
+ * row_start[b] + i sees the rows j < L_b - n_b and the drafted rows k (cached
+ * row L_b - n_b + k) whose bit is set in its mask.  Over those rows
+ *   z_j = softmax_scale * (q_abs[r,h,0:512] . c_j + q_abs[r,h,512:576] . k_j)
+ *   o_lat[r,h,:] = sum_j e^{z_j - m} c_j / sum_j e^{z_j - m},  lse_out[r,h] = m + ln sum_j e^{z_j - m}
+ * A row that sees nothing gets o_lat = 0 and lse_out = -inf.  One row per
+ * sequence (no drafts) is the single-token decode.
+ *   q_abs       device [max_rows, n_heads, 576], q_dtype F32 or BF16
+ *   cache, cache_scale, block_table  as for mla_decode_fwd (its pool contract too:
+ *               rows of a visited page behind the sequence's end and drafted rows
+ *               that a mask hides must hold finite values)
+ *   kv_lens     device int32 [batch];  row_start device int32 [batch + 1], ascending
+ *               from row_start[0] >= 0 to at most max_rows.  A sequence whose numbers
+ *               are impossible (n_b < 0, L_b < n_b, L_b beyond its table row) is
+ *               skipped and flagged MLA_DEVERR_POSITION
+ *   tree_mask   device uint64 [max_rows, mask_words], bit k of word w: drafted row
+ *               64 w + k is seen (bits at or past n_b are ignored, drafted rows past
+ *               the words are not seen); NULL: row i sees the drafted rows 0..i
+ *   workspace   device, mla_decode_tree_workspace_bytes(cache_dtype, max_rows, n_heads)
+ *               bytes, 16-byte aligned, contents need not be kept between calls
+ *   o_lat       device [max_rows, n_heads, 512] of o_dtype (F32 or BF16)
+ *   lse_out     device float [max_rows, n_heads] or NULL
+ *   err_word    device int32 or NULL (MLA_DEVERR_PAGE: rows of a page outside the
+ *               pool are not seen; MLA_DEVERR_POSITION, MLA_DEVERR_TIMEOUT)
+ * Rows of o_lat and lse_out that belong to no sequence are left as they were.
+ * Supported: page_size 64; q F32 with cache F32 (CUDA cores), q BF16 with cache
+ * BF16 or E4M3 (tcgen05 tensor cores, fp32 accumulation).  The softmax weights
+ * enter the value product as bf16 (BF16 cache) or as two e4m3 terms (E4M3
+ * cache, whose queries must be finite); scores, sums and statistics are fp32.
+ * Results do not depend on timing: a call on the same inputs and GPU returns
+ * the same bits.  Calls that share a workspace must not overlap on the GPU, so
+ * two captured graphs that may replay at once need a workspace each.
+ */
+mla_status mla_decode_tree(const void* q_abs, mla_dtype q_dtype, const void* cache, const float* cache_scale,
+                           mla_dtype cache_dtype, int num_pages, const int32_t* block_table, int max_pages_per_seq,
+                           int page_size, const int32_t* kv_lens, const int32_t* row_start, int batch, int max_rows,
+                           int n_heads, const uint64_t* tree_mask, int mask_words, float softmax_scale,
+                           void* workspace, void* o_lat, mla_dtype o_dtype, float* lse_out, int32_t* err_word,
+                           cudaStream_t stream);
+
+/*
+ * mla_cache_commit
+ * Keeps an accepted path of each sequence's drafted rows: with P_b = kv_lens[b]
+ * - n_b rows before the drafts (n_b as in mla_decode_tree), cached row P_b +
+ * i_j moves to row P_b + j for the path's nodes i_0 < i_1 < ..., and
+ *   seq_lens_out[b] = P_b + accept_counts[b]
+ * Rows move as they are: a drafted row's key was rotated to its depth's
+ * position, and the path's j-th node has depth j.  Rows behind the new end keep
+ * what they held.
+ *   kv_lens, row_start  as for mla_decode_tree (mla_step_plan's outputs)
+ *   accept_counts device int32 [batch], each in [0, n_b]
+ *   accept_nodes  device int32 [max_rows]: the path's nodes, ascending, at
+ *                 [row_start[b], row_start[b] + accept_counts[b]); the rest is not read
+ *   block_table, cache, cache_scale as for mla_cache_append; cache is updated
+ *   seq_lens_out  device int32 [batch] or NULL (a model calls this once per layer
+ *                 and needs the lengths once), not one of the inputs
+ *   err_word      device int32 or NULL.  MLA_DEVERR_POSITION: impossible numbers or a
+ *                 path that does not ascend within the tree; the sequence keeps its
+ *                 rows and seq_lens_out[b] = P_b.  MLA_DEVERR_PAGE: a row's page is
+ *                 outside the pool; that row is not moved.
+ */
+mla_status mla_cache_commit(const int32_t* kv_lens, const int32_t* row_start, int batch, int max_rows,
+                            const int32_t* accept_counts, const int32_t* accept_nodes, const int32_t* block_table,
+                            int max_pages_per_seq, int page_size, void* cache, float* cache_scale,
+                            mla_dtype cache_dtype, int num_pages, int32_t* seq_lens_out, int32_t* err_word,
+                            cudaStream_t stream);
 
 /*
  * mla_combine

@@ -17,7 +17,7 @@ LIB_PATH = os.path.join(_PKG, "libmla.so")
 
 MLA_OK, MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA, MLA_ERR_BAD_INDEX, MLA_ERR_TIMEOUT = range(6)
 MLA_F32, MLA_BF16, MLA_E4M3 = 0, 1, 2
-MLA_DEVERR_PAGE, MLA_DEVERR_POSITION, MLA_DEVERR_TIMEOUT = 0x1, 0x2, 0x4
+MLA_DEVERR_PAGE, MLA_DEVERR_POSITION, MLA_DEVERR_TIMEOUT, MLA_DEVERR_CAPACITY = 0x1, 0x2, 0x4, 0x8
 D_C, D_R, D_ROW, D_NOPE, D_V, PAGE = 512, 64, 576, 128, 128, 64
 
 # entry points with their ctypes signatures (p = pointer, i = int, f = float, d = double)
@@ -43,6 +43,11 @@ _SIGS = {
     "mla_decompress_kv": ("i", "piiippipppp"),
     "mla_combine_out_uv": ("i", "ppiiippppp"),
     "mla_attend_naive": ("i", "pppippipiipiiifpppp"),
+    "mla_step_plan": ("i", "pppiiippppppiiipppppppp"),
+    "mla_cache_append_slots": ("i", "piipppfppippiipp"),
+    "mla_decode_tree_workspace_bytes": ("z", "iii"),
+    "mla_decode_tree": ("i", "pippiipiippiiipifppippp"),
+    "mla_cache_commit": ("i", "ppiipppiippiippp"),
 }
 _CT = {"p": ctypes.c_void_p, "i": ctypes.c_int, "f": ctypes.c_float, "d": ctypes.c_double,
        "s": ctypes.c_char_p, "z": ctypes.c_size_t, "Q": ctypes.c_ulonglong}
@@ -174,6 +179,56 @@ def mla_decode_fwd_q8(q8, q_scale, cache, cache_scale, num_pages, block_table, m
         int(max_pages_per_seq), int(page_size), _ptr(seq_lens), int(batch), int(q_len), int(n_heads),
         int(num_splits), int(split_tokens), float(softmax_scale), _ptr(o_part), _ptr(lse_part), _ptr(err_word),
         _stream(stream)))
+
+
+def mla_step_plan(seq_lens, new_counts, parents, batch, max_rows, mask_words, held_in, held_out, free_pages,
+                  free_count_in, free_count_out, block_table, max_pages_per_seq, page_size, num_pages, row_start,
+                  kv_lens, seq_ids, positions, slots, tree_mask, err_word=None, stream=None):
+    """Pages, block table, row offsets, slots, positions and ancestor masks of a
+    step, from device lengths, row counts and drafted trees (parents, seq_ids
+    and tree_mask may be None); tree_mask: int64 [max_rows, mask_words]."""
+    _check("mla_step_plan", lib().mla_step_plan(
+        _ptr(seq_lens), _ptr(new_counts), _ptr(parents), int(batch), int(max_rows), int(mask_words), _ptr(held_in),
+        _ptr(held_out), _ptr(free_pages), _ptr(free_count_in), _ptr(free_count_out), _ptr(block_table),
+        int(max_pages_per_seq), int(page_size), int(num_pages), _ptr(row_start), _ptr(kv_lens), _ptr(seq_ids),
+        _ptr(positions), _ptr(slots), _ptr(tree_mask), _ptr(err_word), _stream(stream)))
+
+
+def mla_cache_append_slots(kv_a, kv_dtype, n_new, slots, positions, norm_gain, eps, rope_cos, rope_sin,
+                           rope_max_pos, cache, cache_scale, cache_dtype, num_pages, err_word=None, stream=None):
+    """mla_cache_append's rows at given slots (-1: skipped), rotated to given positions."""
+    _check("mla_cache_append_slots", lib().mla_cache_append_slots(
+        _ptr(kv_a), int(kv_dtype), int(n_new), _ptr(slots), _ptr(positions), _ptr(norm_gain), float(eps),
+        _ptr(rope_cos), _ptr(rope_sin), int(rope_max_pos), _ptr(cache), _ptr(cache_scale), int(cache_dtype),
+        int(num_pages), _ptr(err_word), _stream(stream)))
+
+
+def mla_decode_tree_workspace_bytes(cache_dtype: int, max_rows: int, n_heads: int) -> int:
+    """Bytes of workspace mla_decode_tree needs."""
+    return int(lib().mla_decode_tree_workspace_bytes(int(cache_dtype), int(max_rows), int(n_heads)))
+
+
+def mla_decode_tree(q_abs, q_dtype, cache, cache_scale, cache_dtype, num_pages, block_table, max_pages_per_seq,
+                    page_size, kv_lens, row_start, batch, max_rows, n_heads, tree_mask, mask_words, softmax_scale,
+                    workspace, o_lat, o_dtype, lse_out=None, err_word=None, stream=None):
+    """Attention and merge of a ragged number of drafted tokens per sequence, each
+    seeing its prefix and the drafted rows of its mask (None: a chain)."""
+    _check("mla_decode_tree", lib().mla_decode_tree(
+        _ptr(q_abs), int(q_dtype), _ptr(cache), _ptr(cache_scale), int(cache_dtype), int(num_pages),
+        _ptr(block_table), int(max_pages_per_seq), int(page_size), _ptr(kv_lens), _ptr(row_start), int(batch),
+        int(max_rows), int(n_heads), _ptr(tree_mask), int(mask_words), float(softmax_scale), _ptr(workspace),
+        _ptr(o_lat), int(o_dtype), _ptr(lse_out), _ptr(err_word), _stream(stream)))
+
+
+def mla_cache_commit(kv_lens, row_start, batch, max_rows, accept_counts, accept_nodes, block_table,
+                     max_pages_per_seq, page_size, cache, cache_scale, cache_dtype, num_pages, seq_lens_out=None,
+                     err_word=None, stream=None):
+    """Move each sequence's accepted path of drafted rows to the front of its
+    drafted rows; seq_lens_out: the lengths after it."""
+    _check("mla_cache_commit", lib().mla_cache_commit(
+        _ptr(kv_lens), _ptr(row_start), int(batch), int(max_rows), _ptr(accept_counts), _ptr(accept_nodes),
+        _ptr(block_table), int(max_pages_per_seq), int(page_size), _ptr(cache), _ptr(cache_scale), int(cache_dtype),
+        int(num_pages), _ptr(seq_lens_out), _ptr(err_word), _stream(stream)))
 
 
 def mla_combine(o_part, lse_part, rows, n_heads, num_splits, o_lat, o_dtype, lse_out=None, stream=None):

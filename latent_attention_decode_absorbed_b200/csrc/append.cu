@@ -28,6 +28,43 @@ __global__ void __launch_bounds__(256) append_kernel(AppendArgs a) {
   append_row<CK>(a, a.seq_ids[warp], a.positions[warp], c, x0, x1, lane);
 }
 
+// The same rows at given slots: a row whose slot is -1 is padding and skipped.
+template <typename IN, int CK>
+__global__ void __launch_bounds__(256) append_slots_kernel(AppendArgs a, const int32_t* __restrict__ slots) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  if (warp >= a.n_new) return;
+  const int slot = slots[warp], p = a.positions[warp];
+  if (slot == -1) return;
+  if (slot < 0 || (slot >> 6) >= a.num_pages) {
+    if (lane == 0) flag_error(a.err, MLA_DEVERR_PAGE);
+    return;
+  }
+  if (p < 0 || p >= a.rope_max_pos) {
+    if (lane == 0) flag_error(a.err, MLA_DEVERR_POSITION);
+    return;
+  }
+  const IN* row = reinterpret_cast<const IN*>(a.kv_a) + (size_t)warp * MLA_D_ROW;
+  float c[16];
+  load16(row + 16 * lane, c);
+  const float x0 = to_f32(row[MLA_D_C + 2 * lane]);
+  const float x1 = to_f32(row[MLA_D_C + 2 * lane + 1]);
+  append_row_at<CK>(a, (size_t)slot, p, c, x0, x1, lane);
+}
+
+template <typename IN>
+cudaError_t launch_slots_in(const AppendArgs& a, const int32_t* slots, cudaStream_t st) {
+  dim3 block(256);
+  dim3 grid((unsigned)(((long long)a.n_new + 7) / 8));
+  switch (a.cache_dtype) {
+    case MLA_F32: return launch_dependent(append_slots_kernel<IN, MLA_F32>, grid, block, 0, st, a, slots);
+    case MLA_BF16: return launch_dependent(append_slots_kernel<IN, MLA_BF16>, grid, block, 0, st, a, slots);
+    default: return launch_dependent(append_slots_kernel<IN, MLA_E4M3>, grid, block, 0, st, a, slots);
+  }
+}
+
 template <typename IN>
 cudaError_t launch_in(const AppendArgs& a, cudaStream_t st) {
   dim3 block(256);
@@ -45,6 +82,12 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t st) {
   if (a.n_new == 0) return cudaSuccess;
   if (a.kv_dtype == MLA_F32) return launch_in<float>(a, st);
   return launch_in<__nv_bfloat16>(a, st);
+}
+
+cudaError_t launch_append_slots(const AppendArgs& a, const int32_t* slots, cudaStream_t st) {
+  if (a.n_new == 0) return cudaSuccess;
+  if (a.kv_dtype == MLA_F32) return launch_slots_in<float>(a, slots, st);
+  return launch_slots_in<__nv_bfloat16>(a, slots, st);
 }
 
 }  // namespace mla

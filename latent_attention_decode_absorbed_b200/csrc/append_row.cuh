@@ -12,22 +12,12 @@
 
 namespace mla {
 
-// c[16]: this lane's latent channels [16 lane, 16 lane + 16) as read;
-// x0, x1: its rope pair (channels 512 + 2 lane, + 1).  s, p: the token's
-// sequence and position.  CK: MLA_F32, MLA_BF16, MLA_E4M3.
+// One row at `slot` of the pool.  c[16]: this lane's latent channels [16 lane,
+// 16 lane + 16) as read; x0, x1: its rope pair (channels 512 + 2 lane, + 1);
+// p: the token's position.  CK: MLA_F32, MLA_BF16, MLA_E4M3.
 template <int CK>
-__device__ __forceinline__ void append_row(const AppendArgs& a, int s, int p, float* c, float x0, float x1,
-                                           int lane) {
-  if (s < 0 || s >= a.batch || p < 0 || p >= a.max_pages * a.page_size || p >= a.rope_max_pos) {
-    if (lane == 0) flag_error(a.err, MLA_DEVERR_POSITION);
-    return;
-  }
-  const int page = a.block_table[(size_t)s * a.max_pages + p / a.page_size];
-  if (page < 0 || page >= a.num_pages) {
-    if (lane == 0) flag_error(a.err, MLA_DEVERR_PAGE);
-    return;
-  }
-  const size_t slot = (size_t)page * a.page_size + (p % a.page_size);
+__device__ __forceinline__ void append_row_at(const AppendArgs& a, size_t slot, int p, float* c, float x0, float x1,
+                                              int lane) {
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) ss = fmaf(c[i], c[i], ss);
@@ -81,6 +71,22 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, int s, int p, fl
     for (int i = 0; i < 4; ++i) d4[i] = make_float4(c[4 * i], c[4 * i + 1], c[4 * i + 2], c[4 * i + 3]);
     *reinterpret_cast<float2*>(dst + cache_index(slot, MLA_D_C + 2 * lane)) = make_float2(r0, r1);
   }
+}
+
+// The same at the slot that the block table gives for position p of sequence s.
+template <int CK>
+__device__ __forceinline__ void append_row(const AppendArgs& a, int s, int p, float* c, float x0, float x1,
+                                           int lane) {
+  if (s < 0 || s >= a.batch || p < 0 || p >= a.max_pages * a.page_size || p >= a.rope_max_pos) {
+    if (lane == 0) flag_error(a.err, MLA_DEVERR_POSITION);
+    return;
+  }
+  const int page = a.block_table[(size_t)s * a.max_pages + p / a.page_size];
+  if (page < 0 || page >= a.num_pages) {
+    if (lane == 0) flag_error(a.err, MLA_DEVERR_PAGE);
+    return;
+  }
+  append_row_at<CK>(a, (size_t)page * a.page_size + (p % a.page_size), p, c, x0, x1, lane);
 }
 
 }  // namespace mla

@@ -1,0 +1,1175 @@
+// Attention of drafted tokens over the paged latent cache, on the tcgen05
+// tensor cores: every drafted token (node) of a sequence sees the sequence's
+// prefix and those drafted rows whose bit is set in its mask.
+//
+// What it computes ("DeepSeek-V2: MLA Explained", "MLA Full Formulas" part 3
+// with the absorption of "Optimization Note").  For node i of sequence b, head
+// h and the rows j that the node sees,
+//   z_j = scale * (q_abs[i,h,0:512] . c_j + q_abs[i,h,512:576] . k_j)
+//   o_lat[i,h,:] = sum_j e^{z_j - m} c_j / sum_j e^{z_j - m},  lse = m + ln sum_j e^{z_j - m}
+//
+// How.  All heads of all nodes of a sequence read the same cached rows, so a
+// sequence's (node, head) pairs are the rows of one dense problem: they are
+// cut into tiles of 128 rows whatever the head count (one node of 128 heads,
+// eight nodes of 16), and per tile of 256 cached rows a CTA pair issues
+//   S[128 x 256]  = Q[128 x 576] . K[256 x 576]^T,   O[128 x 512] += P[128 x 256] . V[256 x 512]
+// exactly as the single-token kernel does for its 128 heads (decode_pair.cu
+// explains the operand layouts, the TMEM layout of M = 128 over a pair, the
+// ring of stages and the softmax's hand-offs).  The mask costs nothing in the
+// prefix: a thread of the softmax owns one row and one 64-row page, and only
+// a page that reaches past the prefix builds a 64-bit visibility word.
+//
+// Work split.  The launch has one persistent CTA pair per SM pair and no
+// split count: the tiles (row tile x cached tile) of all sequences form one
+// list, in (sequence, row tile, cached tile) order, and pair p takes the p-th
+// equal part of it.  Each CTA finds its part by a scan over the sequences'
+// lengths at its start, so lengths stay on the device and a captured graph
+// serves any of them.  A row tile that one pair covers alone is normalised
+// and stored as the final result; a row tile that crosses a pair's border
+// leaves at most two partials per pair (its first and its last segment) in
+// the workspace, which tree_merge_kernel joins.  The partials are thus
+// bounded by the number of pairs, not by the lengths or the batch.
+//
+// With an e4m3 cache both GEMMs run on kind::f8f6f4 straight from the cache
+// codes: the query as two e4m3 terms on a power-of-two scale (split_q_tree
+// below: exact for all but tiny components, so the scores are fp32-exact
+// products), the softmax weights as two e4m3 terms with the row scales
+// folded in relative to a running reference, as in decode_pair.cu.
+#include <math.h>
+
+#include "mla_device.cuh"
+#include "mla_internal.h"
+#include "sm100.cuh"
+
+namespace mla {
+namespace {
+
+using namespace sm100;
+
+constexpr int kTile = 256;                // cached rows per pair tile (128 per CTA)
+constexpr int kM = 128;                   // (node, head) rows per row tile
+constexpr int kHM = 64;                   // of them in one CTA
+constexpr int kChunks = 9;                // 576 / 64 column chunks
+constexpr int kBox = 8192;                // [64 rows x 64 16-bit values]
+constexpr int kBox8 = 4096;               // [64 rows x 64 codes]
+constexpr int kQ8Plane = kChunks * kBox8; // one term (hi or lo) of Q, 9 x [64 rows x 64 codes]
+constexpr int kQChunk = kHM * 128;        // [64 rows x 64 dims], 16-bit
+constexpr int kPChunk = kHM * 128;        // [64 rows x 64 cached rows], 16-bit: P of one page
+constexpr int kWarpProd = 0, kWarpMma = 1, kWarpSoft0 = 2, kSoftWarps = 8;
+constexpr int kThreads = 32 * (kWarpSoft0 + kSoftWarps);
+constexpr float kRescaleLog2 = 8.0f;      // lazy rescale threshold (log2 units)
+constexpr float kRescaleLog2Q8 = 4.0f;    // 8-bit MMAs: probabilities stay <= 2^4, and times
+constexpr float kPScale8 = 16.0f;         // 16 x row scale / reference <= 16 x 1.75 ...
+constexpr float kScaleSlack8 = 1.75f;     // ... the reference is raised past 1.75x: <= 448
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0;             // S of tile t at kColS + 128 (t & 1)
+constexpr uint32_t kColO = 256;           // O: dims 0..255 at 256, dims 256..511 at 384
+
+// offsets inside the misc area
+constexpr int kMBars = 0;                 // 64 barriers
+constexpr int kMTmem = 64 * 8;
+constexpr int kMAbort = kMTmem + 4;
+constexpr int kMRedMax = kMTmem + 16;     // float [2 tile parities][4 parts][64 rows]
+constexpr int kMRedSum = kMRedMax + 2 * 4 * kHM * 4;    // float [4 parts][64 rows]
+constexpr int kMRedSc = kMRedSum + 4 * kHM * 4;         // float [2 tile parities][8 softmax warps]: 8-bit MMAs
+constexpr int kMScan = kMRedSc + 4 * 2 * kSoftWarps;    // int [16]: per-warp sums of the schedule's scan
+constexpr int kMPart = kMScan + 4 * 16;                 // int [4]: this pair's first sequence and its base tile
+constexpr int kMiscBytes = kMPart + 4 * 4;
+
+template <bool D8>
+struct TreeLayout {
+  static constexpr int kSlotB = D8 ? 8192 : 16384;       // bytes of one operand stage
+  static constexpr int kSlots = D8 ? 14 : 7;
+  static constexpr int kOffQ = 0;                        // Q: 9 x 8 KB, K-major SW128 (D8: hi, lo 9 x 4 KB, SW64)
+  static constexpr int kOffRing = kOffQ + kChunks * kQChunk;
+  static constexpr int kOffP = kOffRing + kSlots * kSlotB;   // P: 4 pages x 8 KB (D8: hi, lo 4 KB each)
+  static constexpr int kOffMisc = kOffP + 4 * kPChunk;
+  static constexpr int kSmem = kOffMisc + kMiscBytes + 1024;     // + alignment slack
+  static constexpr int kBFull = 0;                  // [kSlots] leader: a stage is in both CTAs
+  static constexpr int kBEmpty = kSlots;            // [kSlots] both: the MMAs are done with the stage
+  static constexpr int kBSFull = 2 * kSlots;        // [2] both: S of a tile is in TMEM
+  static constexpr int kBODone = kBSFull + 2;       // both: the value MMAs of a tile are done
+  static constexpr int kBPFull = kBODone + 1;       // leader: both CTAs' softmax wrote P (and rescaled O)
+  static constexpr int kBQFull = kBPFull + 1;       // leader: both CTAs' Q landed
+  static constexpr int kBQFree = kBQFull + 1;       // both: the segment's score MMAs are done with Q
+  static constexpr int kBEpiDone = kBQFree + 1;     // leader: both CTAs read O out (TMEM reusable)
+  static constexpr int kBSoft = kBEpiDone + 1;      // local: the softmax warps' own barrier
+  static constexpr int kBEnd = kBSoft + 1;
+  static_assert(kSmem <= 227 * 1024, "shared memory budget");
+  static_assert(kBEnd <= 64, "barrier area");
+};
+
+// A row tile that crosses its pair's border: where its rows go, and how many
+// of the following pairs hold a further part of it (0: nothing to merge).
+struct TreeDesc { int row0, rows, follow, pad; };
+
+struct TreeParams {
+  int n_heads, batch, n_rows;   // n_rows: nodes of the call (capacity of the row arrays)
+  const int32_t* block_table;
+  int max_pages, num_pages;
+  const int32_t* kv_lens;
+  const int32_t* row_start;
+  const uint64_t* tree_mask;    // NULL: node i sees the nodes 0..i
+  int mask_words;
+  float scale_log2;             // softmax_scale * log2(e)
+  const float* cache_scale;     // e4m3 cache: per-row dequantisation scale [num_pages * 64]
+  const float* q_scale;         // 8-bit MMAs: scale of the two-term query per (node, head)
+  float* part_o;                // [2 pairs][128][512]
+  float* part_lse;              // [2 pairs][128]
+  TreeDesc* desc;               // [pairs]
+  void* o_lat;                  // [n_rows, n_heads, 512], bf16 or fp32
+  int o_f32;
+  float* lse;                   // [n_rows, n_heads] or NULL
+  int32_t* err;
+  unsigned long long wait_limit;
+  int withhold_q;
+};
+
+// One sequence's share of the problem; n = 0 (no work) where its numbers are
+// not possible ones.
+struct SeqInfo { int start, n, L, rt, kt; bool bad; };
+
+__device__ __forceinline__ SeqInfo seq_info(const TreeParams& p, int b) {
+  SeqInfo s;
+  const int r0 = p.row_start[b], r1 = p.row_start[b + 1];
+  s.L = p.kv_lens[b];
+  s.start = r0;
+  s.n = r1 - r0;
+  s.bad = r0 < 0 || r1 < r0 || r1 > p.n_rows || s.L < s.n || s.L > p.max_pages * 64;
+  if (s.bad) s.n = 0;
+  s.rt = (s.n * p.n_heads + kM - 1) / kM;
+  s.kt = s.n > 0 ? (s.L + kTile - 1) / kTile : 0;
+  return s;
+}
+
+__device__ __forceinline__ uint64_t low_bits(int n) {   // the n lowest bits, n clamped to [0, 64]
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
+}
+
+// Visibility of the 64 cached rows from `row0` on for one node: bit j set
+// where the node sees row row0 + j.  The prefix is rows 0..prefix-1; drafted
+// row k (cached row prefix + k) is seen where bit k of the node's mask is
+// set, or k <= node without masks.
+__device__ __forceinline__ uint64_t visible_rows(int row0, int prefix, int n, int node, const uint64_t* mask,
+                                                 int words) {
+  const int k0 = row0 - prefix;             // place of the page's first row in the tree
+  if (k0 <= -64) return ~0ull;
+  uint64_t bits;
+  if (!mask) {
+    bits = low_bits(node - k0 + 1);
+    return bits;                            // rows of the prefix (k < 0) are among them
+  }
+  if (k0 < 0) {
+    bits = (mask[0] << (-k0)) | low_bits(-k0);
+  } else {
+    const int w = k0 >> 6, sh = k0 & 63;
+    bits = w < words ? mask[w] >> sh : 0ull;
+    if (sh && w + 1 < words) bits |= mask[w + 1] << (64 - sh);
+  }
+  return bits & low_bits(n - k0);
+}
+
+__device__ __forceinline__ int page_or_minus1(const TreeParams& p, int b, int pidx) {
+  const int pg = pidx < p.max_pages ? p.block_table[(size_t)b * p.max_pages + pidx] : -1;
+  return pg >= 0 && pg < p.num_pages ? pg : -1;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// tm_cache: boxes of one [64 rows x 64 columns] block; tm_cache2: boxes of two
+// adjacent blocks; tm_q: boxes of 64 (node, head) rows x 64 columns.
+template <bool D8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    decode_tree_kernel(const __grid_constant__ CUtensorMap tm_cache, const __grid_constant__ CUtensorMap tm_cache2,
+                       const __grid_constant__ CUtensorMap tm_q, const TreeParams p) {
+  using L = TreeLayout<D8>;
+  constexpr int kSlots = L::kSlots;
+  constexpr int kBFull = L::kBFull, kBEmpty = L::kBEmpty, kBSFull = L::kBSFull, kBODone = L::kBODone,
+                kBPFull = L::kBPFull, kBQFull = L::kBQFull, kBQFree = L::kBQFree, kBEpiDone = L::kBEpiDone,
+                kBSoft = L::kBSoft;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t s_base = smem_u32(smem);
+  const uint32_t s_q = s_base + L::kOffQ, s_ring = s_base + L::kOffRing, s_p = s_base + L::kOffP;
+  uint8_t* misc = smem + L::kOffMisc;
+  uint8_t* s_pbuf = smem + L::kOffP;
+  const uint32_t s_misc = s_base + L::kOffMisc;
+  auto bar = [&](int i) -> uint32_t { return s_misc + kMBars + 8 * i; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + kMAbort);
+  float* red_max = reinterpret_cast<float*>(misc + kMRedMax);
+  float* red_sum = reinterpret_cast<float*>(misc + kMRedSum);
+  float* red_sc = reinterpret_cast<float*>(misc + kMRedSc);
+  int* scan = reinterpret_cast<int*>(misc + kMScan);
+  int* part0 = reinterpret_cast<int*>(misc + kMPart);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t lim = p.wait_limit;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+
+  // ---- set-up
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(bar(kBFull + i), 1);
+      mbar_init(bar(kBEmpty + i), 1);
+    }
+    mbar_init(bar(kBSFull), 1);
+    mbar_init(bar(kBSFull + 1), 1);
+    mbar_init(bar(kBODone), 1);
+    mbar_init(bar(kBPFull), 2 * kSoftWarps);
+    mbar_init(bar(kBQFull), 1);
+    mbar_init(bar(kBQFree), 1);
+    mbar_init(bar(kBEpiDone), 2 * kSoftWarps);
+    mbar_init(bar(kBSoft), kSoftWarps);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpProd) tmem_alloc_pair(s_misc + kMTmem, kTmemCols);
+  // global memory only after the previous kernel on the stream has completed
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // ---- this pair's part [g0, g1) of the list of tiles: a scan over the
+  // sequences' tile counts, each thread a run of consecutive sequences
+  int total, g0, g1, used;
+  {
+    const int per = (p.batch + kThreads - 1) / kThreads;
+    const int b_lo = min(p.batch, (int)threadIdx.x * per), b_hi = min(p.batch, b_lo + per);
+    int sum = 0;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const SeqInfo q = seq_info(p, b);
+      if (q.bad && blockIdx.x == 0) flag_error(p.err, MLA_DEVERR_POSITION);
+      sum += q.rt * q.kt;
+    }
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) scan[warp] = inc;
+    __syncthreads();
+    int before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += scan[w];
+      total += scan[w];
+    }
+    used = min(n_pairs, total);
+    g0 = pair < used ? (int)((long long)pair * total / used) : total;
+    g1 = pair < used ? (int)((long long)(pair + 1) * total / used) : total;
+    int base = before + inc - sum;
+    if (g0 < g1 && base <= g0 && g0 < base + sum) {
+      int b = b_lo;
+      for (;; ++b) {
+        const SeqInfo q = seq_info(p, b);
+        if (g0 < base + q.rt * q.kt) break;
+        base += q.rt * q.kt;
+      }
+      part0[0] = b;
+      part0[1] = base;
+    }
+    if (leader && threadIdx.x == 0) p.desc[pair].follow = 0;   // a segment below may set it
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc + kMTmem);
+
+  // ---- the pair's segments: every role walks the same sequence of them
+  struct Seg { int b, start, n, L, row, k0, nt, kt, g; };
+  struct Walk { int b, base, g; };
+  auto walk_begin = [&]() -> Walk { return Walk{part0[0], part0[1], g0}; };
+  auto next_seg = [&](Walk& w, Seg& s) -> bool {
+    if (w.g >= g1) return false;
+    SeqInfo q = seq_info(p, w.b);
+    while (w.g >= w.base + q.rt * q.kt) {
+      w.base += q.rt * q.kt;
+      q = seq_info(p, ++w.b);
+    }
+    const int at = w.g - w.base, rt = at / q.kt;
+    s.b = w.b;
+    s.start = q.start;
+    s.n = q.n;
+    s.L = q.L;
+    s.row = rt * kM;                       // first (node, head) row of the tile within the sequence
+    s.k0 = at - rt * q.kt;
+    s.kt = q.kt;
+    s.nt = min(q.kt - s.k0, g1 - w.g);
+    s.g = w.g;
+    w.g += s.nt;
+    return true;
+  };
+
+  uint32_t kc = 0;   // ring stages handed out (producer) or consumed (MMA)
+  if (warp == kWarpProd) {
+    // ============ TMA producer (both CTAs), in the order the MMA consumes ============
+    // S(0), then per tile i: S(i+1), O(i); boxes as in decode_pair.cu
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_cache);
+      tma_prefetch_desc(&tm_cache2);
+      tma_prefetch_desc(&tm_q);
+      const uint64_t pol_keep = policy_evict_last();
+      uint32_t uc = 0;
+      bool ok = true;
+      Walk w = walk_begin();
+      Seg s;
+      while (ok && next_seg(w, s)) {
+        // the previous segment's score MMAs must be done with Q (both halves)
+        if (uc > 0) ok = mbar_wait<false>(bar(kBQFree), (uc - 1) & 1, abort_flag, lim);
+        if (!ok) break;
+        // (test hook: the leader leaves the query load of its first segment
+        // out, so the MMA issuer's wait for it runs out and the launch aborts)
+        if (!(p.withhold_q && leader && uc == 0)) {
+          const int row = s.start * p.n_heads + s.row + (int)rank * kHM;
+          const uint32_t q_bar = mapa(bar(kBQFull), 0);
+          if (leader) mbar_arrive_expect_tx(bar(kBQFull), 2u * kChunks * kQChunk);
+          if constexpr (D8) {
+            for (int hl = 0; hl < 2; ++hl)
+              for (int c = 0; c < kChunks; ++c)
+                tma_load_3d_pair(s_q + hl * kQ8Plane + c * kBox8, &tm_q, 64 * c, row, hl, q_bar);
+          } else {
+            for (int c = 0; c < kChunks; ++c) tma_load_2d_pair(s_q + c * kQChunk, &tm_q, 64 * c, row, q_bar);
+          }
+        }
+        const int32_t* bt = p.block_table + (size_t)s.b * p.max_pages;
+        const int pb = 4 * s.k0;      // the segment's first page index
+        auto entry = [&](int pidx) -> int { return pidx < p.max_pages ? bt[pidx] : -1; };
+        // rows outside the table or the pool read page 0 (readable; they are masked)
+        auto page = [&](int pg) -> int { return pg >= 0 && pg < p.num_pages ? pg : 0; };
+        auto take = [&](uint32_t& dst, uint32_t& fb) -> bool {
+          const uint32_t slot = kc % kSlots;
+          const uint32_t ph = (kc / kSlots) & 1u;
+          if (!mbar_wait<false>(bar(kBEmpty + slot), ph ^ 1u, abort_flag, lim)) return false;
+          if (leader) mbar_arrive_expect_tx(bar(kBFull + slot), 2u * L::kSlotB);
+          dst = s_ring + slot * L::kSlotB;
+          fb = mapa(bar(kBFull + slot), 0);
+          ++kc;
+          return true;
+        };
+        // score stages: column chunk c of this CTA's two pages of the tile
+        auto load_s = [&](int pg0, int pg1) -> bool {
+          for (int c = 0; c < kChunks; ++c) {
+            uint32_t dst, fb;
+            if (!take(dst, fb)) return false;
+            tma_load_2d_pair_hint(dst, &tm_cache, 0, (pg0 * kChunks + c) * 64, fb, pol_keep);
+            tma_load_2d_pair_hint(dst + L::kSlotB / 2, &tm_cache, 0, (pg1 * kChunks + c) * 64, fb, pol_keep);
+          }
+          return true;
+        };
+        // value stages: per page of tile j with rows, this CTA's two pairs of dims blocks
+        auto load_o = [&](int j, const int (&pg)[4]) -> bool {
+#pragma unroll
+          for (int pg_i = 0; pg_i < 4; ++pg_i) {
+            if (kTile * (s.k0 + j) + 64 * pg_i >= s.L) break;
+            for (int bb = 0; bb < 2; ++bb) {
+              uint32_t dst, fb;
+              if (!take(dst, fb)) return false;
+              tma_load_2d_pair_hint(dst, &tm_cache2, 0, (pg[pg_i] * kChunks + 4 * bb + 2 * (int)rank) * 64, fb,
+                                    pol_keep);
+            }
+          }
+          return true;
+        };
+        int cur[4], nxt[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          cur[q] = entry(pb + q);
+          nxt[q] = entry(pb + 4 + q);
+        }
+        ok = load_s(page(rank ? cur[2] : cur[0]), page(rank ? cur[3] : cur[1]));
+        for (int i = 0; i < s.nt && ok; ++i) {
+          int ahead[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) ahead[q] = entry(pb + 4 * (i + 2) + q);
+          if (i + 1 < s.nt) ok = load_s(page(rank ? nxt[2] : nxt[0]), page(rank ? nxt[3] : nxt[1]));
+          int pg[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) pg[q] = page(cur[q]);
+          if (ok) ok = load_o(i, pg);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            cur[q] = nxt[q];
+            nxt[q] = ahead[q];
+          }
+        }
+        ++uc;
+      }
+    }
+  } else if (warp == kWarpMma) {
+    // ================= MMA issuer (leader CTA, whole warp, one elected lane) =================
+    if (leader) {
+      constexpr uint32_t idS = D8 ? idesc_e4m3(kM, 256, false, false) : idesc_f16(kM, 256, false, false);
+      constexpr uint32_t idO = D8 ? idesc_e4m3(kM, 256, false, true) : idesc_f16(kM, 256, false, true);
+      auto ready = [&](uint32_t& src, uint32_t& empty) -> bool {
+        const uint32_t slot = kc % kSlots;
+        const uint32_t ph = (kc / kSlots) & 1u;
+        if (!__all_sync(0xffffffffu, mbar_wait<false>(bar(kBFull + slot), ph, abort_flag, lim))) return false;
+        tc_fence_after();
+        src = s_ring + slot * L::kSlotB;
+        empty = bar(kBEmpty + slot);
+        ++kc;
+        return true;
+      };
+      uint32_t uc = 0, gt = 0;
+      bool ok = true;
+      Walk w = walk_begin();
+      Seg s;
+      while (ok && next_seg(w, s)) {
+        ok = __all_sync(0xffffffffu, mbar_wait<false>(bar(kBQFull), uc & 1, abort_flag, lim));
+        if (!ok) break;
+        tc_fence_after();
+        auto issue_s = [&](int i) -> bool {
+          const uint32_t sb = (gt + i) & 1u;
+          const uint32_t d = tmem + kColS + 128 * sb;
+          for (int c = 0; c < kChunks; ++c) {
+            uint32_t a0, empty;
+            if (!ready(a0, empty)) return false;
+            if constexpr (D8) {
+              const uint64_t qd = smem_desc_sw64(s_q, 16, 512);
+              const uint64_t kd = smem_desc_sw64(a0, 16, 512);
+#pragma unroll
+              for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                for (int hl = 0; hl < 2; ++hl)
+                  mma_pair_e4m3_w(d, qd + ((hl * kQ8Plane + c * kBox8 + ks * 32) >> 4), kd + ((ks * 32) >> 4), idS,
+                                  (c | ks | hl) != 0);
+            } else {
+              const uint64_t qd = smem_desc_sw128(s_q, 16, 1024);
+              const uint64_t kd = smem_desc_sw128(a0, 16, 1024);
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)   // K = 16 per MMA: +32 bytes along the 128-byte lines
+                mma_pair_f16_w(d, qd + ((c * kQChunk + ks * 32) >> 4), kd + ((ks * 32) >> 4), idS, (c | ks) != 0);
+            }
+            mma_commit_pair_w(empty, 0x3);
+          }
+          mma_commit_pair_w(bar(kBSFull + sb), 0x3);
+          // the segment's last score GEMM: Q may be replaced once it completes
+          if (i == s.nt - 1) mma_commit_pair_w(bar(kBQFree), 0x3);
+          return true;
+        };
+        auto issue_o = [&](int j) -> bool {
+          const uint32_t t = gt + j;
+          if (!__all_sync(0xffffffffu, mbar_wait<false>(bar(kBPFull), t & 1, abort_flag, lim))) return false;
+          // the accumulator is overwritten by this segment's first value MMA:
+          // the previous segment's epilogue must have read it out
+          if (j == 0 && uc > 0 &&
+              !__all_sync(0xffffffffu, mbar_wait(bar(kBEpiDone), (uc - 1) & 1, abort_flag, lim)))
+            return false;
+          tc_fence_after();
+          for (int pg_i = 0; pg_i < 4; ++pg_i) {
+            if (kTile * (s.k0 + j) + 64 * pg_i >= s.L) break;
+            for (int bb = 0; bb < 2; ++bb) {
+              uint32_t b0, empty;
+              if (!ready(b0, empty)) return false;
+              if constexpr (D8) {
+                const uint64_t pd = smem_desc_sw64(s_p, 16, 512);
+                const uint64_t vd = smem_desc_sw64(b0, kBox8, 512);
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                  for (int hl = 0; hl < 2; ++hl)
+                    mma_pair_e4m3_w(tmem + kColO + 128 * bb, pd + ((pg_i * kPChunk + hl * kBox8 + ks * 32) >> 4),
+                                    vd + ((ks * 2048) >> 4), idO, (j | pg_i | ks | hl) != 0);
+              } else {
+                const uint64_t pd = smem_desc_sw128(s_p, 16, 1024);
+                const uint64_t vd = smem_desc_sw128(b0, kBox, 1024);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)   // 16 rows per MMA: +32 bytes of P lines, +2 KB of V lines
+                  mma_pair_f16_w(tmem + kColO + 128 * bb, pd + ((pg_i * kPChunk + ks * 32) >> 4),
+                                 vd + ((ks * 2048) >> 4), idO, (j | pg_i | ks) != 0);
+              }
+              mma_commit_pair_w(empty, 0x3);
+            }
+          }
+          mma_commit_pair_w(bar(kBODone), 0x3);
+          return true;
+        };
+        ok = issue_s(0);
+        for (int i = 0; i < s.nt && ok; ++i) {
+          if (i + 1 < s.nt) ok = issue_s(i + 1);
+          if (ok) ok = issue_o(i);
+        }
+        gt += s.nt;
+        ++uc;
+      }
+    }
+  } else {
+    // ================= softmax (both CTAs, warps 2-9) =================
+    // Thread (lane quadrant q4, column half ch, lane) owns row hh = 32 (q4 & 1)
+    // + lane of this CTA and the 64 tile rows 128 (q4 >> 1) + 64 ch .. +63.
+    const int q4 = warp & 3;
+    const int half = q4 >> 1;                   // 0: TMEM lanes 0-63, 1: lanes 64-127
+    const int hh = 32 * (q4 & 1) + lane;        // row within this CTA
+    const int ch = (warp - kWarpSoft0) >> 2;    // score columns [64 ch, 64 ch + 64)
+    const uint32_t lane_addr = static_cast<uint32_t>(32 * q4) << 16;
+    const int part = 2 * half + ch;             // which of the row's four partial results (= page of the tile)
+    uint32_t soft_ph = 0;
+    auto soft_sync = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive_local(bar(kBSoft));
+      const bool okk = __all_sync(0xffffffffu, mbar_wait<false>(bar(kBSoft), soft_ph & 1, abort_flag, lim));
+      ++soft_ph;
+      return okk;
+    };
+    uint32_t gt = 0;
+    bool ok = true;
+    Walk w = walk_begin();
+    Seg s;
+    while (ok && next_seg(w, s)) {
+      const int seq_rows = s.n * p.n_heads;
+      const int my = s.row + kHM * (int)rank + hh;            // this thread's (node, head) row of the sequence
+      const int node = min(my, seq_rows - 1) / p.n_heads;     // rows past the end follow the last node
+      const size_t grow = (size_t)s.start * p.n_heads + my;   // ... of the whole call
+      const int prefix = s.L - s.n;
+      const uint64_t* mask = p.tree_mask ? p.tree_mask + (size_t)(s.start + node) * p.mask_words : nullptr;
+      float slq = p.scale_log2, s_ref = 0.f;
+      if constexpr (D8) {
+        if (my < seq_rows) slq *= p.q_scale[grow];
+      }
+      float m_run = -INFINITY, l_acc = 0.f;
+      for (int i = 0; i < s.nt; ++i) {
+        const uint32_t t = gt + i;
+        const uint32_t sb = t & 1u;
+        // cached rows of this thread: one page of the sequence
+        const int row0 = kTile * (s.k0 + i) + 128 * half + 64 * ch;
+        const int nrows = min(max(s.L - row0, 0), 64);
+        uint64_t vis = 0;
+        float sc_lo = 0.f, sc_hi = 0.f;   // e4m3: the page's dequantisation scales (lane l: rows l, l + 32)
+        if (nrows > 0) {
+          const int pg = page_or_minus1(p, s.b, row0 >> 6);
+          if (pg < 0) {
+            flag_error(p.err, MLA_DEVERR_PAGE);
+          } else {
+            vis = visible_rows(row0, prefix, s.n, node, mask, p.mask_words);
+            if constexpr (D8) {
+              if (lane < nrows) sc_lo = p.cache_scale[(size_t)pg * 64 + lane];
+              if (lane + 32 < nrows) sc_hi = p.cache_scale[(size_t)pg * 64 + 32 + lane];
+            }
+          }
+        }
+        const bool full = __all_sync(0xffffffffu, vis == ~0ull);
+        ok = __all_sync(0xffffffffu, mbar_wait<false>(bar(kBSFull + sb), (t >> 1) & 1, abort_flag, lim));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t scol = tmem + lane_addr + kColS + 128 * sb;
+        float v[64];
+        tmem_ld<32>(scol + 64 * ch, v);
+        tmem_ld<32>(scol + 64 * ch + 32, v + 32);
+        tmem_wait_ld();
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 64; ++j) {
+          float sl = slq;
+          if constexpr (D8) sl *= __shfl_sync(0xffffffffu, j < 32 ? sc_lo : sc_hi, j & 31);
+          v[j] *= sl;
+        }
+        if (!full) {
+          const uint32_t vlo = (uint32_t)vis, vhi = (uint32_t)(vis >> 32);
+#pragma unroll
+          for (int j = 0; j < 64; ++j)
+            if (!((j < 32 ? vlo : vhi) >> (j & 31) & 1u)) v[j] = -INFINITY;
+        }
+#pragma unroll
+        for (int j = 0; j < 64; ++j) mx = fmaxf(mx, v[j]);
+        // the four partial maxima of each row, double-buffered by tile parity:
+        // a warp writes the next tile's slot only after passing this tile's
+        // sync, so no warp can overwrite a slot that another is still reading
+        float* rm = red_max + sb * 4 * kHM;
+        rm[part * kHM + hh] = mx;
+        if constexpr (D8) {   // the largest scale of this warp's rows, same buffering
+          float tsm = fmaxf(sc_lo, sc_hi);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) tsm = fmaxf(tsm, __shfl_xor_sync(0xffffffffu, tsm, o));
+          if (lane == 0) red_sc[sb * kSoftWarps + (warp - kWarpSoft0)] = tsm;
+        }
+        if (!(ok = soft_sync())) break;
+        const float tmax = fmaxf(fmaxf(rm[hh], rm[kHM + hh]), fmaxf(rm[2 * kHM + hh], rm[3 * kHM + hh]));
+        const float m_new = (tmax > m_run + (D8 ? kRescaleLog2Q8 : kRescaleLog2)) ? tmax : m_run;
+        const bool changed = m_new != m_run;
+        // factor for the sums and the accumulator kept so far (0 when nothing was kept)
+        const float alpha = (m_run == -INFINITY) ? 0.f : exp2_approx(m_run - m_new);
+        m_run = m_new;
+        const float msub = m_new == -INFINITY ? 0.f : m_new;
+        float w_k = 0.f, s_fac = 1.f;   // D8: weight factor 16 / s_ref; O's factor for a raised s_ref
+        bool s_up = false;
+        if constexpr (D8) {
+          const float* rs = red_sc + sb * kSoftWarps;
+          float tsmax = rs[0];
+#pragma unroll
+          for (int x = 1; x < kSoftWarps; ++x) tsmax = fmaxf(tsmax, rs[x]);
+          if (tsmax > kScaleSlack8 * s_ref) {
+            s_up = s_ref > 0.f;
+            s_fac = s_up ? s_ref / tsmax : 1.f;
+            s_ref = tsmax;
+          }
+          w_k = s_ref > 0.f ? kPScale8 / s_ref : 0.f;
+        }
+        uint32_t pk[32];   // D8: pk[0..15] the hi codes of the 64 rows, pk[16..31] the lo codes
+        float sum = 0.f;
+        if constexpr (D8) {
+          const float wlo = sc_lo * w_k, whi = sc_hi * w_k;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float p0 = exp2_approx(v[2 * j] - msub), p1 = exp2_approx(v[2 * j + 1] - msub);
+            sum += p0 + p1;
+            const float x0 = p0 * __shfl_sync(0xffffffffu, 2 * j < 32 ? wlo : whi, (2 * j) & 31);
+            const float x1 = p1 * __shfl_sync(0xffffffffu, 2 * j + 1 < 32 ? wlo : whi, (2 * j + 1) & 31);
+            uint32_t h2, l2;
+            split_e4m3x2(x0, x1, h2, l2);
+            if (j & 1) {
+              pk[j >> 1] |= h2 << 16;
+              pk[16 + (j >> 1)] |= l2 << 16;
+            } else {
+              pk[j >> 1] = h2;
+              pk[16 + (j >> 1)] = l2;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float p0 = exp2_approx(v[2 * j] - msub), p1 = exp2_approx(v[2 * j + 1] - msub);
+            sum += p0 + p1;
+            pk[j] = pack_bf16(p0, p1);
+          }
+        }
+        l_acc = changed ? fmaf(l_acc, alpha, sum) : l_acc + sum;
+        // every phase of o_done is observed in order (a parity wait cannot
+        // tell a phase two behind from a completed one); O(i-1) done also
+        // frees the P tiles for this tile's probabilities
+        if (i >= 1) {
+          ok = __all_sync(0xffffffffu, mbar_wait<false>(bar(kBODone), (t - 1) & 1, abort_flag, lim));
+          if (!ok) break;
+          tc_fence_after();
+          if (s_up || __any_sync(0xffffffffu, changed)) {
+            const float f = (changed ? alpha : 1.f) * s_fac;
+            const uint32_t oc = tmem + lane_addr + kColO + 128 * ch;
+#pragma unroll 1
+            for (int c4 = 0; c4 < 4; ++c4) {
+              float o[32];
+              tmem_ld<32>(oc + 32 * c4, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] *= f;
+              tmem_st<32>(oc + 32 * c4, o);
+            }
+          }
+        }
+        if constexpr (D8) {
+#pragma unroll
+          for (int hl = 0; hl < 2; ++hl) {
+            uint8_t* line = s_pbuf + part * kPChunk + hl * kBox8 + hh * 64;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<uint4*>(line + ((q ^ ((hh >> 1) & 3)) << 4)) =
+                  make_uint4(pk[16 * hl + 4 * q], pk[16 * hl + 4 * q + 1], pk[16 * hl + 4 * q + 2],
+                             pk[16 * hl + 4 * q + 3]);
+          }
+        } else {
+          uint8_t* line = s_pbuf + part * kPChunk + hh * 128;
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<uint4*>(line + ((q ^ (hh & 7)) << 4)) =
+                make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+        }
+        fence_proxy_async_cta();     // read by the tensor core
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_cta(mapa(bar(kBPFull), 0));
+      }
+      // ---- epilogue: normalise O by the row sums; the final result where the
+      // segment covers the whole row tile, else a partial for the merge
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait<false>(bar(kBODone), (gt + s.nt - 1) & 1, abort_flag, lim));
+      if (ok) {
+        tc_fence_after();
+        red_sum[part * kHM + hh] = l_acc;
+        ok = soft_sync();
+      }
+      if (ok) {
+        const float lt = red_sum[hh] + red_sum[kHM + hh] + red_sum[2 * kHM + hh] + red_sum[3 * kHM + hh];
+        const float inv_l = lt > 0.f ? (D8 ? s_ref / kPScale8 : 1.f) / lt : 0.f;
+        const bool whole = s.nt == s.kt;
+        // a first segment that continues a row tile: slot 2 pair; a last one that leaves its row tile open: 2 pair + 1
+        const int slot = 2 * pair + (s.k0 == 0 ? 1 : 0);
+        if (part == 0) {
+          const float lv = lt > 0.f ? (m_run + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+          if (!whole) p.part_lse[slot * kM + kHM * (int)rank + hh] = lv;
+          else if (p.lse && my < seq_rows) p.lse[grow] = lv;
+        }
+        if (!whole && s.k0 == 0 && leader && part == 0 && hh == 0) {
+          // the pair that holds the row tile's last cached tile: pairs q own [q total / used, ...)
+          const long long end = (long long)s.g + s.kt;
+          const int q_last = (int)((end * used + total - 1) / total) - 1;
+          p.desc[pair] = TreeDesc{s.start * p.n_heads + s.row, min(kM, seq_rows - s.row), q_last - pair, 0};
+        }
+        // this thread's O: dims 256 ch + 128 half + (0..127) of its row, moved
+        // through a 4 KB tile of this warp in the P area (idle until the next
+        // segment's first probabilities, which these warps write), so that a
+        // store instruction covers whole 128-byte lines of four rows
+        const uint32_t oc = tmem + lane_addr + kColO + 128 * ch;
+        uint8_t* tile = s_pbuf + (warp - kWarpSoft0) * 4096;
+        const int rd_row = lane >> 3, rd_q = lane & 7;    // reader: row 4 k + rd_row, 16-byte piece rd_q
+        const int row_w = kHM * (int)rank + 32 * (q4 & 1);    // this warp's first row of the tile
+        const int dim0 = 256 * ch + 128 * half;
+        const int rows_w = min(32, seq_rows - s.row - row_w);   // rows to store (partials: the valid ones too)
+        if (whole && !p.o_f32) {
+          __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o_lat) +
+                               ((size_t)s.start * p.n_heads + s.row + row_w) * MLA_D_C + dim0 + 8 * rd_q;
+#pragma unroll 1
+          for (int c2 = 0; c2 < 2; ++c2) {
+            float o[64];
+            tmem_ld<32>(oc + 64 * c2, o);
+            tmem_ld<32>(oc + 64 * c2 + 32, o + 32);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              *reinterpret_cast<uint4*>(tile + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                  make_uint4(pack_bf16(o[8 * q] * inv_l, o[8 * q + 1] * inv_l),
+                             pack_bf16(o[8 * q + 2] * inv_l, o[8 * q + 3] * inv_l),
+                             pack_bf16(o[8 * q + 4] * inv_l, o[8 * q + 5] * inv_l),
+                             pack_bf16(o[8 * q + 6] * inv_l, o[8 * q + 7] * inv_l));
+            __syncwarp();
+#pragma unroll 4
+            for (int k4 = 0; k4 < 8; ++k4) {
+              const int j = 4 * k4 + rd_row;
+              if (j < rows_w)
+                *reinterpret_cast<uint4*>(dst + (size_t)j * MLA_D_C + 64 * c2) =
+                    *reinterpret_cast<const uint4*>(tile + j * 128 + ((rd_q ^ (j & 7)) << 4));
+            }
+            __syncwarp();
+          }
+        } else {
+          float* base = whole ? reinterpret_cast<float*>(p.o_lat) + ((size_t)s.start * p.n_heads + s.row) * MLA_D_C
+                              : p.part_o + (size_t)slot * kM * MLA_D_C;
+          float* dst = base + (size_t)row_w * MLA_D_C + dim0 + 4 * rd_q;
+#pragma unroll 1
+          for (int c4 = 0; c4 < 4; ++c4) {
+            float o[32];
+            tmem_ld<32>(oc + 32 * c4, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              *reinterpret_cast<float4*>(tile + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                  make_float4(o[4 * q] * inv_l, o[4 * q + 1] * inv_l, o[4 * q + 2] * inv_l, o[4 * q + 3] * inv_l);
+            __syncwarp();
+#pragma unroll 4
+            for (int k4 = 0; k4 < 8; ++k4) {
+              const int j = 4 * k4 + rd_row;
+              if (j < rows_w)
+                *reinterpret_cast<float4*>(dst + (size_t)j * MLA_D_C + 32 * c4) =
+                    *reinterpret_cast<const float4*>(tile + j * 128 + ((rd_q ^ (j & 7)) << 4));
+            }
+            __syncwarp();
+          }
+        }
+        // this warp's part of O has been read: the pair's next segment may overwrite it
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa(bar(kBEpiDone), 0));
+      }
+      gt += s.nt;
+    }
+  }
+
+  // ---- teardown
+  __syncwarp();
+  if (*abort_flag) {
+    if (threadIdx.x == 0) flag_error(p.err, MLA_DEVERR_TIMEOUT);
+    // let copies and MMAs already in flight land before the memory is released
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 2000000ull) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == kWarpProd) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+// Joins the partials of the row tiles that crossed a pair's border: pair p's
+// last segment (slot 2 p + 1) and the first segments (slot 2 q) of the pairs
+// that follow it.  CTA (p, y): rows 4 y .. 4 y + 3 of pair p's row tile, 128
+// threads x 4 channels per row.  Memory-bound: each partial is read once.
+constexpr int kMergeRows = 4;
+
+template <typename OT>
+__global__ void __launch_bounds__(128 * kMergeRows) tree_merge_kernel(const float* __restrict__ part_o,
+                                                                      const float* __restrict__ part_lse,
+                                                                      const TreeDesc* __restrict__ desc,
+                                                                      OT* __restrict__ o_lat,
+                                                                      float* __restrict__ lse_out) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int pair = blockIdx.x;
+  const TreeDesc d = desc[pair];
+  const int j = blockIdx.y * kMergeRows + (threadIdx.x >> 7);
+  const int c = threadIdx.x & 127;
+  if (d.follow == 0 || j >= d.rows) return;
+  auto slot = [&](int k) { return k == 0 ? 2 * pair + 1 : 2 * (pair + k); };
+  float mx = -INFINITY;
+  for (int k = 0; k <= d.follow; ++k) mx = fmaxf(mx, part_lse[slot(k) * kM + j]);
+  float sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (mx != -INFINITY) {
+    for (int k0 = 0; k0 <= d.follow; k0 += 8) {   // eight parts' loads in flight
+      float w[8];
+      float4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const bool in = k0 + k <= d.follow;
+        const int sl = slot(in ? k0 + k : 0);
+        w[k] = in ? expf(part_lse[sl * kM + j] - mx) : 0.f;
+        v[k] = in ? reinterpret_cast<const float4*>(part_o + ((size_t)sl * kM + j) * MLA_D_C)[c]
+                  : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        sum += w[k];
+        acc.x = fmaf(w[k], v[k].x, acc.x);
+        acc.y = fmaf(w[k], v[k].y, acc.y);
+        acc.z = fmaf(w[k], v[k].z, acc.z);
+        acc.w = fmaf(w[k], v[k].w, acc.w);
+      }
+    }
+  }
+  const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+  const size_t row = (size_t)d.row0 + j;
+  OT* dst = o_lat + row * MLA_D_C + 4 * c;
+  dst[0] = from_f32<OT>(acc.x * inv);
+  dst[1] = from_f32<OT>(acc.y * inv);
+  dst[2] = from_f32<OT>(acc.z * inv);
+  dst[3] = from_f32<OT>(acc.w * inv);
+  if (lse_out && c == 0) lse_out[row] = sum > 0.f ? mx + logf(sum) : -INFINITY;
+}
+
+// The two-term e4m3 query of the 8-bit form: per (node, head) vector
+//   scale = 2^(floor(log2 max|q|) - 7),  y = q / scale,  hi = e4m3(y),  lo = e4m3(y - hi)
+// A bf16 value has 8 significant bits and e4m3 has 4: hi takes the upper ones
+// and y - hi, at most half a step of hi, is a whole number of at most 8 of
+// y's own units, so lo holds it exactly unless it falls below e4m3's smallest
+// step 2^-9, i.e. for components under 2^-9 of the largest, whose error is at
+// most 2^-17 of the largest.  A power-of-two scale is what makes it exact.
+// One warp per vector, as in split_q.cu; planes [2][rows][576].
+__global__ void __launch_bounds__(256) split_q_tree_kernel(const __nv_bfloat16* __restrict__ q_abs, int n_vec,
+                                                           uint8_t* __restrict__ q8, float* __restrict__ q_scale) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int vec = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  if (vec >= n_vec) return;
+  const uint32_t* src = reinterpret_cast<const uint32_t*>(q_abs + (size_t)vec * MLA_D_ROW);
+  float2 x[9];
+  float amax = 0.f;
+#pragma unroll
+  for (int k = 0; k < 9; ++k) {
+    const uint32_t w = src[lane + 32 * k];
+    x[k] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+    amax = fmaxf(amax, fmaxf(fabsf(x[k].x), fabsf(x[k].y)));
+  }
+  amax = warp_max(amax);
+  // exponent field of amax, kept where scale and 1 / scale are both normal numbers
+  const int e = min(max((int)(__float_as_uint(amax) >> 23), 8), 253);
+  const float scale = __uint_as_float((uint32_t)(e - 7) << 23);          // 2^(e - 127 - 7)
+  const float inv = __uint_as_float((uint32_t)(254 - (e - 7)) << 23);    // its reciprocal
+  uint16_t* hi = reinterpret_cast<uint16_t*>(q8 + (size_t)vec * MLA_D_ROW);
+  uint16_t* lo = reinterpret_cast<uint16_t*>(q8 + ((size_t)n_vec + vec) * MLA_D_ROW);
+#pragma unroll
+  for (int k = 0; k < 9; ++k) {
+    uint32_t h2, l2;
+    split_e4m3x2(x[k].x * inv, x[k].y * inv, h2, l2);
+    hi[lane + 32 * k] = (uint16_t)h2;
+    lo[lane + 32 * k] = (uint16_t)l2;
+  }
+  if (lane == 0) q_scale[vec] = scale;
+}
+
+// ------------------------------------------------------------------ fp32 cache
+// Exact fp32 on the CUDA cores, for small models: CTA = (split of the
+// sequence's rows, group of 16 heads, node), one warp per head, rows staged 32
+// at a time in shared memory; lane l owns channels l + 32 k.  Each sequence is
+// cut into `splits` equal runs of whole 32-row groups, so few nodes still
+// fill the GPU; tree_merge_f32_kernel joins the splits.
+constexpr int kSimtRows = 32;
+constexpr int kSimtHeads = 16;
+
+// The sequence of node n: the largest b with row_start[b] <= n (-1: n lies
+// outside [row_start[0], row_start[batch]), or the sequence's numbers are bad).
+__device__ __forceinline__ int seq_of(const TreeParams& p, int n, SeqInfo& s) {
+  if (n < p.row_start[0] || n >= p.row_start[p.batch]) return -1;
+  int lo = 0, hi = p.batch - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.row_start[mid] <= n) lo = mid; else hi = mid - 1;
+  }
+  s = seq_info(p, lo);
+  return s.bad || n < s.start || n >= s.start + s.n ? -1 : lo;
+}
+
+__global__ void __launch_bounds__(32 * kSimtHeads) decode_tree_simt_kernel(const float* __restrict__ q_abs,
+                                                                           const float* __restrict__ cache,
+                                                                           TreeParams p, int splits) {
+  extern __shared__ float tile[];            // [kSimtRows][576]
+  __shared__ long long slot_of[kSimtRows];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int split = blockIdx.x, n = blockIdx.z;
+  SeqInfo s;
+  const int b = seq_of(p, n, s);
+  if (b < 0) {
+    if (threadIdx.x == 0 && n >= p.row_start[0] && n < p.row_start[p.batch]) flag_error(p.err, MLA_DEVERR_POSITION);
+    return;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = blockIdx.y * kSimtHeads + warp;
+  const bool active = h < p.n_heads;
+  const int node = n - s.start, prefix = s.L - s.n;
+  const int groups = (s.L + kSimtRows - 1) / kSimtRows;
+  const int lo = (int)((long long)groups * split / splits) * kSimtRows;
+  const int hi = min((int)((long long)groups * (split + 1) / splits) * kSimtRows, s.L);
+  const uint64_t* mask = p.tree_mask ? p.tree_mask + (size_t)n * p.mask_words : nullptr;
+  const size_t vec = (size_t)n * p.n_heads + (active ? h : 0);
+  float q[18];
+#pragma unroll
+  for (int k = 0; k < 18; ++k) q[k] = q_abs[vec * MLA_D_ROW + lane + 32 * k];
+  float m = -INFINITY, l = 0.f;
+  float o[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) o[k] = 0.f;
+  for (int j0 = lo; j0 < hi; j0 += kSimtRows) {
+    const int cnt = min(kSimtRows, hi - j0);
+    __syncthreads();
+    if (threadIdx.x < kSimtRows) {
+      long long sl = -1;
+      if ((int)threadIdx.x < cnt) {
+        const int j = j0 + threadIdx.x;
+        const int pg = page_or_minus1(p, b, j >> 6);
+        if (pg >= 0) sl = (long long)pg * 64 + (j & 63);
+        else flag_error(p.err, MLA_DEVERR_PAGE);
+      }
+      slot_of[threadIdx.x] = sl;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < cnt * (MLA_D_ROW / 4); i += blockDim.x) {
+      const int jj = i / (MLA_D_ROW / 4), d = 4 * (i % (MLA_D_ROW / 4));
+      const long long sl = slot_of[jj];
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (sl >= 0) x = *reinterpret_cast<const float4*>(cache + cache_index((size_t)sl, d));
+      *reinterpret_cast<float4*>(tile + jj * MLA_D_ROW + d) = x;
+    }
+    __syncthreads();
+    if (!active) continue;
+    // lane jj holds row j0 + jj's score
+    const int k0 = j0 & ~63;
+    const uint64_t vis = visible_rows(k0, prefix, s.n, node, mask, p.mask_words);
+    const bool seen = lane < cnt && slot_of[lane] >= 0 && ((vis >> (j0 - k0 + lane)) & 1);
+    float sc = -INFINITY;
+    for (int jj = 0; jj < cnt; ++jj) {
+      float part = 0.f;
+#pragma unroll
+      for (int k = 0; k < 18; ++k) part = fmaf(q[k], tile[jj * MLA_D_ROW + lane + 32 * k], part);
+      part = warp_sum(part);
+      if (lane == jj && seen) sc = part * p.scale_log2;   // natural scale here, see the launch
+    }
+    const float mn = fmaxf(m, warp_max(sc));
+    if (mn == -INFINITY) continue;          // the node sees no row of the group
+    const float alpha = expf(m - mn);
+    const float pr = expf(sc - mn);
+    l = l * alpha + warp_sum(pr);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) o[k] *= alpha;
+    for (int jj = 0; jj < cnt; ++jj) {
+      const float pj = __shfl_sync(0xffffffffu, pr, jj);
+      if (pj == 0.f) continue;              // masked rows are not touched (0 times infinity would be NaN)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) o[k] = fmaf(pj, tile[jj * MLA_D_ROW + lane + 32 * k], o[k]);
+    }
+    m = mn;
+  }
+  if (!active) return;
+  const size_t base = vec * splits + split;
+  const float inv = l > 0.f ? 1.0f / l : 0.f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) p.part_o[base * MLA_D_C + lane + 32 * k] = o[k] * inv;
+  if (lane == 0) p.part_lse[base] = l > 0.f ? m + logf(l) : -INFINITY;
+}
+
+template <typename OT>
+__global__ void __launch_bounds__(128) tree_merge_f32_kernel(TreeParams p, int splits) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const size_t vec = blockIdx.x;
+  SeqInfo s;
+  if (seq_of(p, (int)(vec / p.n_heads), s) < 0) return;
+  const float* lp = p.part_lse + vec * splits;
+  float mx = -INFINITY;
+  for (int k = 0; k < splits; ++k) mx = fmaxf(mx, lp[k]);
+  float sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (mx != -INFINITY) {
+    for (int k = 0; k < splits; ++k) {
+      const float w = expf(lp[k] - mx);
+      const float4 v = reinterpret_cast<const float4*>(p.part_o + (vec * splits + k) * MLA_D_C)[threadIdx.x];
+      sum += w;
+      acc.x = fmaf(w, v.x, acc.x);
+      acc.y = fmaf(w, v.y, acc.y);
+      acc.z = fmaf(w, v.z, acc.z);
+      acc.w = fmaf(w, v.w, acc.w);
+    }
+  }
+  const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+  OT* dst = reinterpret_cast<OT*>(p.o_lat) + vec * MLA_D_C + 4 * threadIdx.x;
+  dst[0] = from_f32<OT>(acc.x * inv);
+  dst[1] = from_f32<OT>(acc.y * inv);
+  dst[2] = from_f32<OT>(acc.z * inv);
+  dst[3] = from_f32<OT>(acc.w * inv);
+  if (p.lse && threadIdx.x == 0) p.lse[vec] = sum > 0.f ? mx + logf(sum) : -INFINITY;
+}
+
+// ------------------------------------------------------------------ host side
+constexpr long long kMaxPairs = 96;     // bound of the workspace's partials, whatever the GPU's SM count
+constexpr int kMaxSplitsF32 = 16;
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Workspace: tensor-core forms [partials o][partials lse][descriptors], e4m3 also
+// [query planes][query scales]; fp32 [partials o][partials lse].
+struct TreeWorkspace { size_t lse, desc, q8, q_scale, bytes; };
+
+TreeWorkspace tree_workspace(int cache_dtype, long long rows, int n_heads) {
+  TreeWorkspace w{};
+  const size_t vec = (size_t)rows * n_heads;
+  if (cache_dtype == MLA_F32) {
+    w.lse = up256(vec * kMaxSplitsF32 * MLA_D_C * sizeof(float));
+    w.bytes = w.lse + up256(vec * kMaxSplitsF32 * sizeof(float));
+    return w;
+  }
+  w.lse = (size_t)2 * kMaxPairs * kM * MLA_D_C * sizeof(float);
+  w.desc = w.lse + up256((size_t)2 * kMaxPairs * kM * sizeof(float));
+  w.q8 = w.desc + up256(kMaxPairs * sizeof(TreeDesc));
+  w.q_scale = w.q8;
+  w.bytes = w.q8;
+  if (cache_dtype == MLA_E4M3) {
+    w.q_scale = w.q8 + up256(2 * vec * MLA_D_ROW);
+    w.bytes = w.q_scale + up256(vec * sizeof(float));
+  }
+  return w;
+}
+
+bool encode(TensorMapEncodeFn enc, CUtensorMap* m, CUtensorMapDataType t, int rank, const void* base,
+            const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle sw) {
+  const cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, t, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool D8>
+cudaError_t launch_tc(const TreeArgs& a, TreeParams p, const void* q8, cudaStream_t st) {
+  TensorMapEncodeFn enc = tensor_map_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  CUtensorMap tc, tc2, tq;
+  const cuuint64_t elt = D8 ? 1 : 2;
+  const CUtensorMapDataType type = D8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUtensorMapSwizzle sw = D8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  // the page-blocked pool as 2-D [num_pages * 9 * 64 lines x 64 columns]:
+  // boxes of one block (64 lines) and of two adjacent blocks
+  for (int k = 0; k < 2; ++k) {
+    const cuuint64_t dims[2] = {64, (cuuint64_t)a.num_pages * kChunks * 64};
+    const cuuint64_t strides[1] = {64 * elt};
+    const cuuint32_t box[2] = {64, k == 0 ? 64u : 128u};
+    if (!encode(enc, k == 0 ? &tc : &tc2, type, 2, a.cache, dims, strides, box, sw)) return cudaErrorInvalidValue;
+  }
+  // the queries as [(node, head) rows x 576] (8-bit: two planes of it): boxes
+  // of 64 rows x 64 columns, rows past the end read as zeros
+  {
+    const cuuint64_t vec = (cuuint64_t)a.rows * a.n_heads;
+    const cuuint64_t dims[3] = {MLA_D_ROW, vec, 2};
+    const cuuint64_t strides[2] = {MLA_D_ROW * elt, vec * MLA_D_ROW};
+    const cuuint32_t box[3] = {64, (cuuint32_t)kHM, 1};
+    if (!encode(enc, &tq, type, D8 ? 3 : 2, D8 ? q8 : a.q_abs, dims, strides, box, sw)) return cudaErrorInvalidValue;
+  }
+  const int smem = TreeLayout<D8>::kSmem;
+  cudaError_t e = cudaFuncSetAttribute(decode_tree_kernel<D8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  // no more pairs than tiles there can be
+  const long long most = (((long long)a.rows * a.n_heads + kM - 1) / kM + a.batch) *
+                         (((long long)a.max_pages * 64 + kTile - 1) / kTile);
+  long long pairs = sm_pair_count();
+  if (pairs > kMaxPairs) pairs = kMaxPairs;
+  if (pairs > most) pairs = most;
+  e = launch_dependent(decode_tree_kernel<D8>, dim3((unsigned)(2 * pairs)), dim3(kThreads), smem, st, tc, tc2, tq, p);
+  if (e != cudaSuccess || pairs == 1) return e;    // one pair leaves no partials
+  const dim3 grid((unsigned)pairs, kM / kMergeRows);
+  if (a.o_dtype == MLA_F32)
+    return launch_dependent(tree_merge_kernel<float>, grid, dim3(128 * kMergeRows), 0, st, p.part_o, p.part_lse,
+                            p.desc, static_cast<float*>(p.o_lat), p.lse);
+  return launch_dependent(tree_merge_kernel<__nv_bfloat16>, grid, dim3(128 * kMergeRows), 0, st, p.part_o, p.part_lse,
+                          p.desc, static_cast<__nv_bfloat16*>(p.o_lat), p.lse);
+}
+
+}  // namespace
+
+size_t decode_tree_workspace_bytes(int cache_dtype, long long rows, int n_heads) {
+  return tree_workspace(cache_dtype, rows, n_heads).bytes;
+}
+
+cudaError_t launch_decode_tree(const TreeArgs& a, cudaStream_t st) {
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  const TreeWorkspace w = tree_workspace(a.cache_dtype, a.rows, a.n_heads);
+  TreeParams p{};
+  p.n_heads = a.n_heads;
+  p.batch = a.batch;
+  p.n_rows = a.rows;
+  p.block_table = a.block_table;
+  p.max_pages = a.max_pages;
+  p.num_pages = a.num_pages;
+  p.kv_lens = a.kv_lens;
+  p.row_start = a.row_start;
+  p.tree_mask = a.tree_mask;
+  p.mask_words = a.mask_words;
+  p.cache_scale = a.cache_scale;
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_lse = reinterpret_cast<float*>(ws + w.lse);
+  p.o_lat = a.o_lat;
+  p.o_f32 = a.o_dtype == MLA_F32;
+  p.lse = a.lse;
+  p.err = a.err;
+  if (a.cache_dtype == MLA_F32) {
+    p.scale_log2 = a.softmax_scale;    // this form works in natural units
+    const long long groups = ((long long)a.max_pages * 64 + kSimtRows - 1) / kSimtRows;
+    const int splits = (int)(groups < kMaxSplitsF32 ? groups : kMaxSplitsF32);
+    const int smem = kSimtRows * MLA_D_ROW * (int)sizeof(float);
+    cudaError_t e = cudaFuncSetAttribute(decode_tree_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)splits, (unsigned)((a.n_heads + kSimtHeads - 1) / kSimtHeads), (unsigned)a.rows);
+    e = launch_dependent(decode_tree_simt_kernel, grid, dim3(32 * kSimtHeads), smem, st,
+                         static_cast<const float*>(a.q_abs), static_cast<const float*>(a.cache), p, splits);
+    if (e != cudaSuccess) return e;
+    const dim3 mg((unsigned)((long long)a.rows * a.n_heads));
+    if (a.o_dtype == MLA_F32) return launch_dependent(tree_merge_f32_kernel<float>, mg, dim3(128), 0, st, p, splits);
+    return launch_dependent(tree_merge_f32_kernel<__nv_bfloat16>, mg, dim3(128), 0, st, p, splits);
+  }
+  p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
+  p.desc = reinterpret_cast<TreeDesc*>(ws + w.desc);
+  p.wait_limit = g_wait_limit.load();
+  p.withhold_q = g_withhold_q.load();
+  if (a.cache_dtype == MLA_BF16) return launch_tc<false>(a, p, nullptr, st);
+  uint8_t* q8 = ws + w.q8;
+  p.q_scale = reinterpret_cast<float*>(ws + w.q_scale);
+  const int n_vec = a.rows * a.n_heads;
+  const cudaError_t e =
+      launch_dependent(split_q_tree_kernel, dim3((unsigned)(((long long)n_vec + 7) / 8)), dim3(256), 0, st,
+                       static_cast<const __nv_bfloat16*>(a.q_abs), n_vec, q8, reinterpret_cast<float*>(ws + w.q_scale));
+  if (e != cudaSuccess) return e;
+  return launch_tc<true>(a, p, q8, st);
+}
+
+}  // namespace mla

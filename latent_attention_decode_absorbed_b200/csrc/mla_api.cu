@@ -51,7 +51,7 @@ const char* mla_status_string(int status) {
 
 const char* mla_last_error_message(void) { return g_msg; }
 
-int mla_version(void) { return 10000; }
+int mla_version(void) { return 10100; }
 
 size_t mla_decode_workspace_bytes(int batch, int q_len, int n_heads, int num_splits) {
   if (batch <= 0 || q_len <= 0 || n_heads <= 0 || num_splits <= 0) return 0;
@@ -212,6 +212,132 @@ mla_status mla_decode_fwd_q8(const void* q8, const float* q_scale, const void* c
                o_part, lse_part, err_word, q_scale};
   MLA_REQUIRE(decode_pair_supported(a), MLA_ERR_UNSUPPORTED, "mla_decode_fwd_q8: unsupported sizes");
   return cuda_status(launch_decode_pair(a, stream), "mla_decode_fwd_q8 launch (tcgen05 kind::f8f6f4, head-split pairs)");
+}
+
+mla_status mla_step_plan(const int32_t* seq_lens, const int32_t* new_counts, const int32_t* parents, int batch,
+                         int max_rows, int mask_words, const int32_t* held_in, int32_t* held_out, int32_t* free_pages,
+                         const int32_t* free_count_in, int32_t* free_count_out, int32_t* block_table,
+                         int max_pages_per_seq, int page_size, int num_pages, int32_t* row_start, int32_t* kv_lens,
+                         int32_t* seq_ids, int32_t* positions, int32_t* slots, uint64_t* tree_mask,
+                         int32_t* err_word, cudaStream_t stream) {
+  MLA_REQUIRE(page_size == MLA_PAGE, MLA_ERR_UNSUPPORTED, "mla_step_plan: page_size must be %d", MLA_PAGE);
+  MLA_REQUIRE(batch >= 1 && max_rows >= 0 && max_pages_per_seq >= 1 && num_pages >= 1, MLA_ERR_INVALID_ARG,
+              "mla_step_plan: batch, max_pages_per_seq, num_pages must be >= 1 and max_rows >= 0");
+  MLA_REQUIRE(mask_words >= 0 && (!tree_mask || mask_words >= 1), MLA_ERR_INVALID_ARG,
+              "mla_step_plan: mask_words must be >= 1 with a tree_mask, else >= 0");
+  MLA_REQUIRE((long long)max_pages_per_seq * page_size < (1ll << 31) && (long long)num_pages * page_size < (1ll << 31) &&
+                  (long long)batch * max_pages_per_seq < (1ll << 31),
+              MLA_ERR_UNSUPPORTED, "mla_step_plan: table or pool beyond int32 slots");
+  MLA_REQUIRE(seq_lens && new_counts && held_in && held_out && free_pages && free_count_in && free_count_out &&
+                  block_table && row_start && kv_lens && (max_rows == 0 || (positions && slots)),
+              MLA_ERR_INVALID_ARG, "mla_step_plan: null pointer");
+  MLA_REQUIRE(kv_lens != seq_lens && kv_lens != new_counts && row_start != seq_lens && row_start != new_counts &&
+                  held_out != seq_lens && held_out != new_counts,
+              MLA_ERR_INVALID_ARG, "mla_step_plan: only held and free_count may be updated in place");
+  PlanArgs a{seq_lens, new_counts, parents, batch, max_rows, mask_words, held_in, held_out, free_pages, free_count_in,
+             free_count_out, block_table, max_pages_per_seq, num_pages, row_start, kv_lens, seq_ids, positions, slots,
+             tree_mask, err_word};
+  return cuda_status(launch_step_plan(a, stream), "mla_step_plan launch");
+}
+
+mla_status mla_cache_append_slots(const void* kv_a, mla_dtype kv_dtype, int n_new, const int32_t* slots,
+                                  const int32_t* positions, const float* norm_gain, float eps, const float* rope_cos,
+                                  const float* rope_sin, int rope_max_pos, void* cache, float* cache_scale,
+                                  mla_dtype cache_dtype, int num_pages, int32_t* err_word, cudaStream_t stream) {
+  MLA_REQUIRE(n_new >= 0, MLA_ERR_INVALID_ARG, "mla_cache_append_slots: n_new < 0");
+  MLA_REQUIRE(kv_dtype == MLA_F32 || kv_dtype == MLA_BF16, MLA_ERR_UNSUPPORTED,
+              "mla_cache_append_slots: kv_dtype must be F32 or BF16");
+  MLA_REQUIRE(cache_dtype == MLA_F32 || cache_dtype == MLA_BF16 || cache_dtype == MLA_E4M3, MLA_ERR_UNSUPPORTED,
+              "mla_cache_append_slots: bad cache_dtype");
+  MLA_REQUIRE(num_pages >= 1 && rope_max_pos >= 1, MLA_ERR_INVALID_ARG,
+              "mla_cache_append_slots: num_pages and rope_max_pos must be >= 1");
+  MLA_REQUIRE((long long)num_pages * MLA_PAGE < (1ll << 31), MLA_ERR_UNSUPPORTED,
+              "mla_cache_append_slots: pool beyond int32 slots");
+  MLA_REQUIRE(eps >= 0.f && isfinite(eps), MLA_ERR_INVALID_ARG,
+              "mla_cache_append_slots: eps must be finite and >= 0");
+  if (n_new == 0) return MLA_OK;
+  MLA_REQUIRE(kv_a && slots && positions && rope_cos && rope_sin && cache, MLA_ERR_INVALID_ARG,
+              "mla_cache_append_slots: null pointer");
+  MLA_REQUIRE(cache_dtype != MLA_E4M3 || cache_scale, MLA_ERR_INVALID_ARG,
+              "mla_cache_append_slots: E4M3 cache needs cache_scale");
+  MLA_REQUIRE(aligned(kv_a, 16) && aligned(cache, 16) && aligned(norm_gain, 16), MLA_ERR_INVALID_ARG,
+              "mla_cache_append_slots: kv_a, cache and norm_gain must be 16-byte aligned");
+  AppendArgs a{kv_a, kv_dtype, n_new, nullptr, positions, nullptr, 0, 0, MLA_PAGE, norm_gain, eps, rope_cos, rope_sin,
+               rope_max_pos, cache, cache_scale, cache_dtype, num_pages, err_word};
+  return cuda_status(launch_append_slots(a, slots, stream), "mla_cache_append_slots launch");
+}
+
+size_t mla_decode_tree_workspace_bytes(mla_dtype cache_dtype, int max_rows, int n_heads) {
+  if (max_rows <= 0 || n_heads <= 0 || n_heads > MLA_MAX_HEADS ||
+      (cache_dtype != MLA_F32 && cache_dtype != MLA_BF16 && cache_dtype != MLA_E4M3))
+    return 0;
+  return decode_tree_workspace_bytes(cache_dtype, max_rows, n_heads);
+}
+
+mla_status mla_decode_tree(const void* q_abs, mla_dtype q_dtype, const void* cache, const float* cache_scale,
+                           mla_dtype cache_dtype, int num_pages, const int32_t* block_table, int max_pages_per_seq,
+                           int page_size, const int32_t* kv_lens, const int32_t* row_start, int batch, int max_rows,
+                           int n_heads, const uint64_t* tree_mask, int mask_words, float softmax_scale,
+                           void* workspace, void* o_lat, mla_dtype o_dtype, float* lse_out, int32_t* err_word,
+                           cudaStream_t stream) {
+  MLA_REQUIRE(page_size == MLA_PAGE, MLA_ERR_UNSUPPORTED, "mla_decode_tree: page_size must be %d", MLA_PAGE);
+  MLA_REQUIRE(batch >= 1 && max_rows >= 0 && num_pages >= 1 && max_pages_per_seq >= 1, MLA_ERR_INVALID_ARG,
+              "mla_decode_tree: batch, num_pages, max_pages_per_seq must be >= 1 and max_rows >= 0");
+  MLA_REQUIRE(n_heads >= 1 && n_heads <= MLA_MAX_HEADS, MLA_ERR_INVALID_ARG,
+              "mla_decode_tree: n_heads must be in [1, %d]", MLA_MAX_HEADS);
+  MLA_REQUIRE(!tree_mask || mask_words >= 1, MLA_ERR_INVALID_ARG, "mla_decode_tree: mask_words must be >= 1");
+  MLA_REQUIRE(isfinite(softmax_scale) && softmax_scale > 0.f, MLA_ERR_INVALID_ARG,
+              "mla_decode_tree: softmax_scale must be finite and > 0");
+  MLA_REQUIRE((q_dtype == MLA_F32 && cache_dtype == MLA_F32) ||
+                  (q_dtype == MLA_BF16 && (cache_dtype == MLA_BF16 || cache_dtype == MLA_E4M3)),
+              MLA_ERR_UNSUPPORTED, "mla_decode_tree: supported (q, cache) dtypes are (F32, F32), (BF16, BF16), (BF16, E4M3)");
+  MLA_REQUIRE(o_dtype == MLA_F32 || o_dtype == MLA_BF16, MLA_ERR_UNSUPPORTED,
+              "mla_decode_tree: o_dtype must be F32 or BF16");
+  MLA_REQUIRE((long long)max_pages_per_seq * page_size < (1ll << 31), MLA_ERR_INVALID_ARG,
+              "mla_decode_tree: table capacity overflows int32 positions");
+  // the work list's index (tiles of 128 (node, head) rows x 256 cached rows) and the fp32 form's grid
+  MLA_REQUIRE((((long long)max_rows * n_heads + 127) / 128 + batch) * ((long long)max_pages_per_seq / 4 + 1) < (1ll << 31) &&
+                  (long long)max_rows * n_heads < (1ll << 28),
+              MLA_ERR_UNSUPPORTED, "mla_decode_tree: too many rows for one call");
+  MLA_REQUIRE(cache_dtype != MLA_F32 || max_rows <= 65535, MLA_ERR_UNSUPPORTED,
+              "mla_decode_tree: more than 65535 rows over an F32 cache");
+  if (max_rows == 0) return MLA_OK;
+  MLA_REQUIRE(q_abs && cache && block_table && kv_lens && row_start && workspace && o_lat, MLA_ERR_INVALID_ARG,
+              "mla_decode_tree: null pointer");
+  MLA_REQUIRE(cache_dtype != MLA_E4M3 || cache_scale, MLA_ERR_INVALID_ARG,
+              "mla_decode_tree: E4M3 cache needs cache_scale");
+  MLA_REQUIRE(aligned(q_abs, 16) && aligned(cache, 128) && aligned(workspace, 16) && aligned(o_lat, 16) &&
+                  aligned(tree_mask, 8),
+              MLA_ERR_INVALID_ARG,
+              "mla_decode_tree: q_abs, workspace and o_lat must be 16-byte aligned, tree_mask 8-byte, cache 128-byte");
+  TreeArgs a{q_abs, cache, cache_scale, cache_dtype, num_pages, block_table, max_pages_per_seq, kv_lens, row_start,
+             batch, max_rows, n_heads, tree_mask, mask_words, softmax_scale, workspace, o_lat, o_dtype, lse_out, err_word};
+  return cuda_status(launch_decode_tree(a, stream), "mla_decode_tree launch");
+}
+
+mla_status mla_cache_commit(const int32_t* kv_lens, const int32_t* row_start, int batch, int max_rows,
+                            const int32_t* accept_counts, const int32_t* accept_nodes, const int32_t* block_table,
+                            int max_pages_per_seq, int page_size, void* cache, float* cache_scale,
+                            mla_dtype cache_dtype, int num_pages, int32_t* seq_lens_out, int32_t* err_word,
+                            cudaStream_t stream) {
+  MLA_REQUIRE(page_size == MLA_PAGE, MLA_ERR_UNSUPPORTED, "mla_cache_commit: page_size must be %d", MLA_PAGE);
+  MLA_REQUIRE(batch >= 1 && max_rows >= 0 && num_pages >= 1 && max_pages_per_seq >= 1, MLA_ERR_INVALID_ARG,
+              "mla_cache_commit: batch, num_pages, max_pages_per_seq must be >= 1 and max_rows >= 0");
+  MLA_REQUIRE(cache_dtype == MLA_F32 || cache_dtype == MLA_BF16 || cache_dtype == MLA_E4M3, MLA_ERR_UNSUPPORTED,
+              "mla_cache_commit: bad cache_dtype");
+  MLA_REQUIRE((long long)max_pages_per_seq * page_size < (1ll << 31), MLA_ERR_INVALID_ARG,
+              "mla_cache_commit: table capacity overflows int32 positions");
+  MLA_REQUIRE(kv_lens && row_start && accept_counts && accept_nodes && block_table && cache, MLA_ERR_INVALID_ARG,
+              "mla_cache_commit: null pointer");
+  MLA_REQUIRE(seq_lens_out != kv_lens && seq_lens_out != accept_counts && seq_lens_out != row_start,
+              MLA_ERR_INVALID_ARG, "mla_cache_commit: seq_lens_out must be a buffer of its own");
+  MLA_REQUIRE(cache_dtype != MLA_E4M3 || cache_scale, MLA_ERR_INVALID_ARG,
+              "mla_cache_commit: E4M3 cache needs cache_scale");
+  MLA_REQUIRE(aligned(cache, 16), MLA_ERR_INVALID_ARG, "mla_cache_commit: cache must be 16-byte aligned");
+  CommitArgs a{kv_lens, row_start, batch, max_rows, accept_counts, accept_nodes, block_table, max_pages_per_seq, cache,
+               cache_dtype == MLA_E4M3 ? cache_scale : nullptr,
+               cache_dtype == MLA_F32 ? 4 : cache_dtype == MLA_BF16 ? 2 : 1, num_pages, seq_lens_out, err_word};
+  return cuda_status(launch_cache_commit(a, stream), "mla_cache_commit launch");
 }
 
 mla_status mla_out_proj(const void* out, const void* w_o, float* u, int rows, int n_heads, int d_model,

@@ -26,6 +26,30 @@ struct AppendArgs {
   int32_t* err;
 };
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t st);
+// the same rows at given slots (seq_ids, block_table, batch and max_pages unused)
+cudaError_t launch_append_slots(const AppendArgs& a, const int32_t* slots, cudaStream_t st);
+
+// the pages, table, offsets, slots, positions and masks of a step
+struct PlanArgs {
+  const int32_t* seq_lens; const int32_t* new_counts; const int32_t* parents;
+  int batch; int max_rows; int mask_words;
+  const int32_t* held_in; int32_t* held_out;
+  int32_t* free_pages; const int32_t* free_count_in; int32_t* free_count_out;
+  int32_t* block_table; int max_pages; int num_pages;
+  int32_t* row_start; int32_t* kv_lens; int32_t* seq_ids; int32_t* positions; int32_t* slots; uint64_t* mask;
+  int32_t* err;
+};
+cudaError_t launch_step_plan(const PlanArgs& a, cudaStream_t st);
+
+// an accepted path's rows moved to the front of the drafted rows
+struct CommitArgs {
+  const int32_t* kv_lens; const int32_t* row_start; int batch; int n_rows;
+  const int32_t* counts; const int32_t* nodes;
+  const int32_t* block_table; int max_pages;
+  void* cache; float* cache_scale; int elt; int num_pages;   // elt: bytes per cached number
+  int32_t* seq_lens; int32_t* err;
+};
+cudaError_t launch_cache_commit(const CommitArgs& a, cudaStream_t st);
 
 // the two-term e4m3 form of bf16 absorbed queries (see mla_split_q_e4m3)
 cudaError_t launch_split_q_e4m3(const void* q_abs, int rows, int n_heads, void* q8, float* q_scale, cudaStream_t st);
@@ -55,6 +79,19 @@ cudaError_t launch_decode_pair(const DecodeArgs& a, cudaStream_t st);
 // tcgen05 path: bf16 queries over a bf16 or e4m3 cache
 bool decode_tc_supported(const DecodeArgs& a);
 cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t st);
+
+// attention of drafted tokens over the paged cache (bf16 queries over a bf16
+// or e4m3 cache, fp32 over fp32)
+struct TreeArgs {
+  const void* q_abs;
+  const void* cache; const float* cache_scale; int cache_dtype; int num_pages;
+  const int32_t* block_table; int max_pages;
+  const int32_t* kv_lens; const int32_t* row_start; int batch; int rows; int n_heads;
+  const uint64_t* tree_mask; int mask_words; float softmax_scale;
+  void* workspace; void* o_lat; int o_dtype; float* lse; int32_t* err;
+};
+size_t decode_tree_workspace_bytes(int cache_dtype, long long rows, int n_heads);
+cudaError_t launch_decode_tree(const TreeArgs& a, cudaStream_t st);
 
 // split-K tcgen05 GEMMs of the projections around the attention core
 cudaError_t launch_out_proj(const void* out_heads, const void* w_o, float* u, int rows, int n_heads, int d_model,
