@@ -366,8 +366,9 @@ mla_status mla_cache_append_slots(const void* kv_a, mla_dtype kv_dtype, int n_ne
  * mla_decode_tree_workspace_bytes (host function, no GPU needed)
  * Bytes of caller workspace mla_decode_tree needs for a call of max_rows rows
  * with this cache: for bf16 a fixed 50 MB of fp32 partials, for e4m3 also
- * 1156 bytes per (row, head) for the two-term query, for fp32 32.8 KB per
- * (row, head).  0 for non-positive sizes or an unknown dtype.
+ * 1156 bytes per (row, head) for the two-term query, for fp32 2052 bytes per
+ * (row, head) and split (the fewer rows, the more splits, at most 64).
+ * 0 for non-positive sizes or an unknown dtype.
  */
 size_t mla_decode_tree_workspace_bytes(mla_dtype cache_dtype, int max_rows, int n_heads);
 

@@ -29,35 +29,72 @@ __global__ void __launch_bounds__(256) append_kernel(AppendArgs a) {
 }
 
 // The same rows at given slots: a row whose slot is -1 is padding and skipped.
+// Prompts bring tens of thousands of rows, and one row is a chain of loads
+// (slot and position, then the row and its rope table line), two reductions
+// and a store.  So a warp walks rows a grid apart and holds the next row's
+// loads in flight while it works on this one's; the gains stay in registers.
+template <typename IN>
+struct RawRow {
+  uint4 v[sizeof(IN)];        // 16 channels
+  IN x[2];                    // the rope pair
+  int slot, pos;
+};
+template <typename IN>
+__device__ __forceinline__ RawRow<IN> load_raw(const AppendArgs& a, const int32_t* slots, int r, int lane) {
+  RawRow<IN> w;
+  w.slot = -1;
+  w.pos = 0;
+  if (r >= a.n_new) return w;
+  w.slot = slots[r];
+  w.pos = a.positions[r];
+  const IN* row = reinterpret_cast<const IN*>(a.kv_a) + (size_t)r * MLA_D_ROW;
+  const uint4* src = reinterpret_cast<const uint4*>(row + 16 * lane);
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(IN); ++i) w.v[i] = __ldcs(src + i);
+  if constexpr (sizeof(IN) == 4)
+    *reinterpret_cast<float2*>(w.x) = *reinterpret_cast<const float2*>(row + MLA_D_C + 2 * lane);
+  else
+    *reinterpret_cast<uint32_t*>(w.x) = *reinterpret_cast<const uint32_t*>(row + MLA_D_C + 2 * lane);
+  return w;
+}
+
 template <typename IN, int CK>
 __global__ void __launch_bounds__(256) append_slots_kernel(AppendArgs a, const int32_t* __restrict__ slots) {
   griddep_wait();
   griddep_launch_dependents();
-  const int warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
-  if (warp >= a.n_new) return;
-  const int slot = slots[warp], p = a.positions[warp];
-  if (slot == -1) return;
-  if (slot < 0 || (slot >> 6) >= a.num_pages) {
-    if (lane == 0) flag_error(a.err, MLA_DEVERR_PAGE);
-    return;
+  const int stride = (gridDim.x * blockDim.x) >> 5;
+  int r = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  RawRow<IN> cur = load_raw<IN>(a, slots, r, lane);
+  float g[16];
+  load_gain(a, lane, g);
+  for (; r < a.n_new; r += stride) {
+    const RawRow<IN> next = load_raw<IN>(a, slots, r + stride, lane);
+    const int slot = cur.slot, p = cur.pos;
+    if (slot != -1) {
+      if (slot < 0 || (slot >> 6) >= a.num_pages) {
+        if (lane == 0) flag_error(a.err, MLA_DEVERR_PAGE);
+      } else if (p < 0 || p >= a.rope_max_pos) {
+        if (lane == 0) flag_error(a.err, MLA_DEVERR_POSITION);
+      } else {
+        const float cs = a.rope_cos[(size_t)p * (MLA_D_R / 2) + lane];
+        const float sn = a.rope_sin[(size_t)p * (MLA_D_R / 2) + lane];
+        float c[16];
+        load16(reinterpret_cast<const IN*>(cur.v), c);
+        store_row<CK>(a, (size_t)slot, c, to_f32(cur.x[0]), to_f32(cur.x[1]), g, cs, sn, lane);
+      }
+    }
+    cur = next;
   }
-  if (p < 0 || p >= a.rope_max_pos) {
-    if (lane == 0) flag_error(a.err, MLA_DEVERR_POSITION);
-    return;
-  }
-  const IN* row = reinterpret_cast<const IN*>(a.kv_a) + (size_t)warp * MLA_D_ROW;
-  float c[16];
-  load16(row + 16 * lane, c);
-  const float x0 = to_f32(row[MLA_D_C + 2 * lane]);
-  const float x1 = to_f32(row[MLA_D_C + 2 * lane + 1]);
-  append_row_at<CK>(a, (size_t)slot, p, c, x0, x1, lane);
 }
 
 template <typename IN>
 cudaError_t launch_slots_in(const AppendArgs& a, const int32_t* slots, cudaStream_t st) {
-  dim3 block(256);
-  dim3 grid((unsigned)(((long long)a.n_new + 7) / 8));
+  // one row per warp while that fits the GPU, else a grid that fills it
+  long long ctas = ((long long)a.n_new + 7) / 8;
+  const long long most = 2 * sm_pair_count() * 3;
+  if (ctas > most) ctas = most;
+  const dim3 block(256), grid((unsigned)ctas);
   switch (a.cache_dtype) {
     case MLA_F32: return launch_dependent(append_slots_kernel<IN, MLA_F32>, grid, block, 0, st, a, slots);
     case MLA_BF16: return launch_dependent(append_slots_kernel<IN, MLA_BF16>, grid, block, 0, st, a, slots);

@@ -14,10 +14,11 @@ namespace mla {
 
 // One row at `slot` of the pool.  c[16]: this lane's latent channels [16 lane,
 // 16 lane + 16) as read; x0, x1: its rope pair (channels 512 + 2 lane, + 1);
-// p: the token's position.  CK: MLA_F32, MLA_BF16, MLA_E4M3.
+// g[16]: the gains of its channels (1 without a gain); cs, sn: cos and sin of
+// its pair at the token's position.  CK: MLA_F32, MLA_BF16, MLA_E4M3.
 template <int CK>
-__device__ __forceinline__ void append_row_at(const AppendArgs& a, size_t slot, int p, float* c, float x0, float x1,
-                                              int lane) {
+__device__ __forceinline__ void store_row(const AppendArgs& a, size_t slot, float* c, float x0, float x1,
+                                          const float* g, float cs, float sn, int lane) {
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) ss = fmaf(c[i], c[i], ss);
@@ -25,12 +26,7 @@ __device__ __forceinline__ void append_row_at(const AppendArgs& a, size_t slot, 
   const float rms = sqrtf(ss * (1.0f / MLA_D_C) + a.eps);
   const float inv = 1.0f / rms;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    float g = a.gain ? a.gain[16 * lane + i] : 1.0f;
-    c[i] = (c[i] * inv) * g;
-  }
-  const float cs = a.rope_cos[(size_t)p * (MLA_D_R / 2) + lane];
-  const float sn = a.rope_sin[(size_t)p * (MLA_D_R / 2) + lane];
+  for (int i = 0; i < 16; ++i) c[i] = (c[i] * inv) * g[i];
   const float r0 = __fsub_rn(__fmul_rn(x0, cs), __fmul_rn(x1, sn));
   const float r1 = __fadd_rn(__fmul_rn(x0, sn), __fmul_rn(x1, cs));
   if constexpr (CK == MLA_E4M3) {
@@ -73,7 +69,17 @@ __device__ __forceinline__ void append_row_at(const AppendArgs& a, size_t slot, 
   }
 }
 
-// The same at the slot that the block table gives for position p of sequence s.
+// The gains of this lane's 16 channels.
+__device__ __forceinline__ void load_gain(const AppendArgs& a, int lane, float* g) {
+  if (a.gain) {
+    load16(a.gain + 16 * lane, g);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) g[i] = 1.0f;
+  }
+}
+
+// The row of position p of sequence s, at the slot that the block table gives.
 template <int CK>
 __device__ __forceinline__ void append_row(const AppendArgs& a, int s, int p, float* c, float x0, float x1,
                                            int lane) {
@@ -86,7 +92,10 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, int s, int p, fl
     if (lane == 0) flag_error(a.err, MLA_DEVERR_PAGE);
     return;
   }
-  append_row_at<CK>(a, (size_t)page * a.page_size + (p % a.page_size), p, c, x0, x1, lane);
+  float g[16];
+  load_gain(a, lane, g);
+  store_row<CK>(a, (size_t)page * a.page_size + (p % a.page_size), c, x0, x1, g,
+                a.rope_cos[(size_t)p * (MLA_D_R / 2) + lane], a.rope_sin[(size_t)p * (MLA_D_R / 2) + lane], lane);
 }
 
 }  // namespace mla

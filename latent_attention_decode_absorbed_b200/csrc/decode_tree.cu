@@ -894,18 +894,22 @@ __global__ void __launch_bounds__(256) split_q_tree_kernel(const __nv_bfloat16* 
 
 // ------------------------------------------------------------------ fp32 cache
 // Exact fp32 on the CUDA cores, for small models: CTA = (split of the
-// sequence's rows, group of 16 heads, node), one warp per head, rows staged 32
-// at a time in shared memory; lane l owns channels l + 32 k.  Each sequence is
-// cut into `splits` equal runs of whole 32-row groups, so few nodes still
-// fill the GPU; tree_merge_f32_kernel joins the splits.
+// sequence's rows, group of 16 heads, node), two heads per warp so that a row
+// read from shared memory serves both; rows staged 32 at a time.  Each sequence
+// is cut into `splits` equal runs of whole 8-row groups: a call of few nodes
+// still fills the GPU, down to one group per CTA, since what bounds it is the
+// latency of a CTA's chain of loads, products and reductions.
+// tree_merge_f32_kernel joins the splits.
 constexpr int kSimtRows = 32;
+constexpr int kSimtGroup = 8;
 constexpr int kSimtHeads = 16;
+constexpr int kSimtWarps = kSimtHeads / 2;
 
-// The sequence of node n: the largest b with row_start[b] <= n (-1: n lies
-// outside [row_start[0], row_start[batch]), or the sequence's numbers are bad).
+// The sequence of node n (-1: n lies outside [row_start[0], row_start[batch]),
+// or the sequence's numbers are bad).
 __device__ __forceinline__ int seq_of(const TreeParams& p, int n, SeqInfo& s) {
   if (n < p.row_start[0] || n >= p.row_start[p.batch]) return -1;
-  int lo = 0, hi = p.batch - 1;
+  int lo = 0, hi = p.batch - 1;             // the last sequence that starts at or before n
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (p.row_start[mid] <= n) lo = mid; else hi = mid - 1;
@@ -914,11 +918,33 @@ __device__ __forceinline__ int seq_of(const TreeParams& p, int n, SeqInfo& s) {
   return s.bad || n < s.start || n >= s.start + s.n ? -1 : lo;
 }
 
-__global__ void __launch_bounds__(32 * kSimtHeads) decode_tree_simt_kernel(const float* __restrict__ q_abs,
+// Sums of eight values over the warp: the value of index lane >> 2, on every lane.
+__device__ __forceinline__ float warp_sum8(const float (&v)[8]) {
+  const int lane = threadIdx.x & 31;
+  float a[4], b[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool up = lane & 16;
+    a[i] = (up ? v[i + 4] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 4], 16);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const bool up = lane & 8;
+    b[i] = (up ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, up ? a[i] : a[i + 2], 8);
+  }
+  const bool up = lane & 4;
+  float c = (up ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, up ? b[0] : b[1], 4);
+  c += __shfl_xor_sync(0xffffffffu, c, 2);
+  c += __shfl_xor_sync(0xffffffffu, c, 1);
+  return c;
+}
+
+__global__ void __launch_bounds__(32 * kSimtWarps) decode_tree_simt_kernel(const float* __restrict__ q_abs,
                                                                            const float* __restrict__ cache,
                                                                            TreeParams p, int splits) {
   extern __shared__ float tile[];            // [kSimtRows][576]
   __shared__ long long slot_of[kSimtRows];
+  __shared__ float score[kSimtWarps][2][kSimtRows];
   griddep_wait();
   griddep_launch_dependents();
   const int split = blockIdx.x, n = blockIdx.z;
@@ -929,21 +955,25 @@ __global__ void __launch_bounds__(32 * kSimtHeads) decode_tree_simt_kernel(const
     return;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y * kSimtHeads + warp;
-  const bool active = h < p.n_heads;
+  const int h0 = blockIdx.y * kSimtHeads + 2 * warp;
+  const int heads = min(max(p.n_heads - h0, 0), 2);      // of this warp
   const int node = n - s.start, prefix = s.L - s.n;
-  const int groups = (s.L + kSimtRows - 1) / kSimtRows;
-  const int lo = (int)((long long)groups * split / splits) * kSimtRows;
-  const int hi = min((int)((long long)groups * (split + 1) / splits) * kSimtRows, s.L);
+  const int groups = (s.L + kSimtGroup - 1) / kSimtGroup;
+  const int lo = (int)((long long)groups * split / splits) * kSimtGroup;
+  const int hi = min((int)((long long)groups * (split + 1) / splits) * kSimtGroup, s.L);
   const uint64_t* mask = p.tree_mask ? p.tree_mask + (size_t)n * p.mask_words : nullptr;
-  const size_t vec = (size_t)n * p.n_heads + (active ? h : 0);
-  float q[18];
+  const size_t vec = (size_t)n * p.n_heads + h0;
+  float q[2][18];
 #pragma unroll
-  for (int k = 0; k < 18; ++k) q[k] = q_abs[vec * MLA_D_ROW + lane + 32 * k];
-  float m = -INFINITY, l = 0.f;
-  float o[16];
+  for (int e = 0; e < 2; ++e)
 #pragma unroll
-  for (int k = 0; k < 16; ++k) o[k] = 0.f;
+    for (int k = 0; k < 18; ++k) q[e][k] = e < heads ? q_abs[(vec + e) * MLA_D_ROW + lane + 32 * k] : 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float o[2][16];
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+#pragma unroll
+    for (int k = 0; k < 16; ++k) o[e][k] = 0.f;
   for (int j0 = lo; j0 < hi; j0 += kSimtRows) {
     const int cnt = min(kSimtRows, hi - j0);
     __syncthreads();
@@ -958,7 +988,8 @@ __global__ void __launch_bounds__(32 * kSimtHeads) decode_tree_simt_kernel(const
       slot_of[threadIdx.x] = sl;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < cnt * (MLA_D_ROW / 4); i += blockDim.x) {
+    const int cnt4 = (cnt + 3) & ~3;         // rows are worked four at a time: the rest as zeros
+    for (int i = threadIdx.x; i < cnt4 * (MLA_D_ROW / 4); i += blockDim.x) {
       const int jj = i / (MLA_D_ROW / 4), d = 4 * (i % (MLA_D_ROW / 4));
       const long long sl = slot_of[jj];
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -966,40 +997,61 @@ __global__ void __launch_bounds__(32 * kSimtHeads) decode_tree_simt_kernel(const
       *reinterpret_cast<float4*>(tile + jj * MLA_D_ROW + d) = x;
     }
     __syncthreads();
-    if (!active) continue;
-    // lane jj holds row j0 + jj's score
-    const int k0 = j0 & ~63;
-    const uint64_t vis = visible_rows(k0, prefix, s.n, node, mask, p.mask_words);
-    const bool seen = lane < cnt && slot_of[lane] >= 0 && ((vis >> (j0 - k0 + lane)) & 1);
-    float sc = -INFINITY;
-    for (int jj = 0; jj < cnt; ++jj) {
-      float part = 0.f;
+    if (heads == 0) continue;
+    for (int jj = 0; jj < cnt4; jj += 4) {
+      float part[8];                         // [head][row]
 #pragma unroll
-      for (int k = 0; k < 18; ++k) part = fmaf(q[k], tile[jj * MLA_D_ROW + lane + 32 * k], part);
-      part = warp_sum(part);
-      if (lane == jj && seen) sc = part * p.scale_log2;   // natural scale here, see the launch
+      for (int x = 0; x < 8; ++x) part[x] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 18; ++k) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float t = tile[(jj + x) * MLA_D_ROW + lane + 32 * k];
+          part[x] = fmaf(q[0][k], t, part[x]);
+          part[4 + x] = fmaf(q[1][k], t, part[4 + x]);
+        }
+      }
+      const float v = warp_sum8(part);
+      if ((lane & 3) == 0) score[warp][lane >> 4][jj + ((lane >> 2) & 3)] = v;
     }
-    const float mn = fmaxf(m, warp_max(sc));
-    if (mn == -INFINITY) continue;          // the node sees no row of the group
-    const float alpha = expf(m - mn);
-    const float pr = expf(sc - mn);
-    l = l * alpha + warp_sum(pr);
+    __syncwarp();
+    const uint64_t vis = visible_rows(j0, prefix, s.n, node, mask, p.mask_words);
+    const bool seen = lane < cnt && slot_of[lane] >= 0 && ((vis >> lane) & 1);   // row j0 + lane
+    float pr[2];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) o[k] *= alpha;
-    for (int jj = 0; jj < cnt; ++jj) {
-      const float pj = __shfl_sync(0xffffffffu, pr, jj);
-      if (pj == 0.f) continue;              // masked rows are not touched (0 times infinity would be NaN)
+    for (int e = 0; e < 2; ++e) {
+      const float sc = seen ? score[warp][e][lane] * p.scale_log2 : -INFINITY;   // natural units here, see the launch
+      const float mn = fmaxf(m[e], warp_max(sc));
+      const float ms = mn == -INFINITY ? 0.f : mn;      // nothing seen so far: every weight is 0
+      const float alpha = expf(m[e] - ms);
+      pr[e] = expf(sc - ms);
+      l[e] = l[e] * alpha + warp_sum(pr[e]);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) o[k] = fmaf(pj, tile[jj * MLA_D_ROW + lane + 32 * k], o[k]);
+      for (int k = 0; k < 16; ++k) o[e][k] *= alpha;
+      m[e] = mn;
     }
-    m = mn;
+    __syncwarp();
+    const uint32_t any = __ballot_sync(0xffffffffu, seen);
+    for (int jj = 0; jj < cnt; ++jj) {
+      if (!(any >> jj & 1)) continue;       // hidden rows are not touched (0 times infinity would be NaN)
+      const float p0 = __shfl_sync(0xffffffffu, pr[0], jj), p1 = __shfl_sync(0xffffffffu, pr[1], jj);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float t = tile[jj * MLA_D_ROW + lane + 32 * k];
+        o[0][k] = fmaf(p0, t, o[0][k]);
+        o[1][k] = fmaf(p1, t, o[1][k]);
+      }
+    }
   }
-  if (!active) return;
-  const size_t base = vec * splits + split;
-  const float inv = l > 0.f ? 1.0f / l : 0.f;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) p.part_o[base * MLA_D_C + lane + 32 * k] = o[k] * inv;
-  if (lane == 0) p.part_lse[base] = l > 0.f ? m + logf(l) : -INFINITY;
+  for (int e = 0; e < 2; ++e) {
+    if (e >= heads) break;
+    const size_t base = (vec + e) * splits + split;
+    const float inv = l[e] > 0.f ? 1.0f / l[e] : 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) p.part_o[base * MLA_D_C + lane + 32 * k] = o[e][k] * inv;
+    if (lane == 0) p.part_lse[base] = l[e] > 0.f ? m[e] + logf(l[e]) : -INFINITY;
+  }
 }
 
 template <typename OT>
@@ -1010,19 +1062,31 @@ __global__ void __launch_bounds__(128) tree_merge_f32_kernel(TreeParams p, int s
   SeqInfo s;
   if (seq_of(p, (int)(vec / p.n_heads), s) < 0) return;
   const float* lp = p.part_lse + vec * splits;
+  const int lane = threadIdx.x & 31;
+  const float4* op = reinterpret_cast<const float4*>(p.part_o + vec * splits * MLA_D_C) + threadIdx.x;
   float mx = -INFINITY;
-  for (int k = 0; k < splits; ++k) mx = fmaxf(mx, lp[k]);
+  for (int k = lane; k < splits; k += 32) mx = fmaxf(mx, lp[k]);
+  mx = warp_max(mx);
   float sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   if (mx != -INFINITY) {
-    for (int k = 0; k < splits; ++k) {
-      const float w = expf(lp[k] - mx);
-      const float4 v = reinterpret_cast<const float4*>(p.part_o + (vec * splits + k) * MLA_D_C)[threadIdx.x];
-      sum += w;
-      acc.x = fmaf(w, v.x, acc.x);
-      acc.y = fmaf(w, v.y, acc.y);
-      acc.z = fmaf(w, v.z, acc.z);
-      acc.w = fmaf(w, v.w, acc.w);
+    for (int k0 = 0; k0 < splits; k0 += 8) {     // eight parts' loads in flight
+      float w[8];
+      float4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int at = min(k0 + k, splits - 1);
+        w[k] = k0 + k < splits ? expf(lp[at] - mx) : 0.f;
+        v[k] = op[(size_t)at * (MLA_D_C / 4)];
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        sum += w[k];
+        acc.x = fmaf(w[k], v[k].x, acc.x);
+        acc.y = fmaf(w[k], v[k].y, acc.y);
+        acc.z = fmaf(w[k], v[k].z, acc.z);
+        acc.w = fmaf(w[k], v[k].w, acc.w);
+      }
     }
   }
   const float inv = sum > 0.f ? 1.0f / sum : 0.f;
@@ -1036,7 +1100,13 @@ __global__ void __launch_bounds__(128) tree_merge_f32_kernel(TreeParams p, int s
 
 // ------------------------------------------------------------------ host side
 constexpr long long kMaxPairs = 96;     // bound of the workspace's partials, whatever the GPU's SM count
-constexpr int kMaxSplitsF32 = 16;
+
+// Splits of the fp32 form: enough CTAs for four per SM of a B200, at most 64.
+int splits_f32(long long rows, int n_heads) {
+  const long long ctas = rows * ((n_heads + kSimtHeads - 1) / kSimtHeads);
+  const long long want = (4 * 148 + ctas - 1) / ctas;
+  return (int)(want < 64 ? want : 64);
+}
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -1048,8 +1118,9 @@ TreeWorkspace tree_workspace(int cache_dtype, long long rows, int n_heads) {
   TreeWorkspace w{};
   const size_t vec = (size_t)rows * n_heads;
   if (cache_dtype == MLA_F32) {
-    w.lse = up256(vec * kMaxSplitsF32 * MLA_D_C * sizeof(float));
-    w.bytes = w.lse + up256(vec * kMaxSplitsF32 * sizeof(float));
+    const size_t splits = (size_t)splits_f32(rows, n_heads);
+    w.lse = up256(vec * splits * MLA_D_C * sizeof(float));
+    w.bytes = w.lse + up256(vec * splits * sizeof(float));
     return w;
   }
   w.lse = (size_t)2 * kMaxPairs * kM * MLA_D_C * sizeof(float);
@@ -1144,13 +1215,14 @@ cudaError_t launch_decode_tree(const TreeArgs& a, cudaStream_t st) {
   p.err = a.err;
   if (a.cache_dtype == MLA_F32) {
     p.scale_log2 = a.softmax_scale;    // this form works in natural units
-    const long long groups = ((long long)a.max_pages * 64 + kSimtRows - 1) / kSimtRows;
-    const int splits = (int)(groups < kMaxSplitsF32 ? groups : kMaxSplitsF32);
+    const long long groups = (long long)a.max_pages * (64 / kSimtGroup);
+    int splits = splits_f32(a.rows, a.n_heads);
+    if (splits > groups) splits = (int)groups;
     const int smem = kSimtRows * MLA_D_ROW * (int)sizeof(float);
     cudaError_t e = cudaFuncSetAttribute(decode_tree_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)splits, (unsigned)((a.n_heads + kSimtHeads - 1) / kSimtHeads), (unsigned)a.rows);
-    e = launch_dependent(decode_tree_simt_kernel, grid, dim3(32 * kSimtHeads), smem, st,
+    e = launch_dependent(decode_tree_simt_kernel, grid, dim3(32 * kSimtWarps), smem, st,
                          static_cast<const float*>(a.q_abs), static_cast<const float*>(a.cache), p, splits);
     if (e != cudaSuccess) return e;
     const dim3 mg((unsigned)((long long)a.rows * a.n_heads));

@@ -32,25 +32,34 @@ __device__ __forceinline__ Sums add(const Sums& a, const Sums& b) {
   return Sums{a.rows + b.rows, a.take + b.take, a.give + b.give};
 }
 
-// Exclusive prefix of each thread's sums within the CTA, and the CTA's total.
-__device__ __forceinline__ Sums block_scan(const Sums& mine, Sums* warp_sums, Sums& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Sums inc = mine;
+__device__ __forceinline__ Sums warp_scan(Sums v) {   // inclusive
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    Sums v{__shfl_up_sync(0xffffffffu, inc.rows, o), __shfl_up_sync(0xffffffffu, inc.take, o),
-           __shfl_up_sync(0xffffffffu, inc.give, o)};
-    if (lane >= o) inc = add(inc, v);
+    const Sums u{__shfl_up_sync(0xffffffffu, v.rows, o), __shfl_up_sync(0xffffffffu, v.take, o),
+                 __shfl_up_sync(0xffffffffu, v.give, o)};
+    if (lane >= o) v = add(v, u);
   }
+  return v;
+}
+__device__ __forceinline__ Sums from_lane(const Sums& v, int lane) {
+  return Sums{__shfl_sync(0xffffffffu, v.rows, lane), __shfl_sync(0xffffffffu, v.take, lane),
+              __shfl_sync(0xffffffffu, v.give, lane)};
+}
+
+// Exclusive prefix of each thread's sums within the CTA, and the CTA's total.
+// Every warp scans the warps' sums for itself: one barrier fewer than a
+// second level in one warp, and no loop over 32 of them.
+__device__ __forceinline__ Sums block_scan(const Sums& mine, Sums* warp_sums, Sums& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Sums inc = warp_scan(mine);
   __syncthreads();                       // the previous use of warp_sums is over
   if (lane == 31) warp_sums[warp] = inc;
   __syncthreads();
-  Sums before{0, 0, 0};
-  total = Sums{0, 0, 0};
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before = add(before, warp_sums[w]);
-    total = add(total, warp_sums[w]);
-  }
+  const Sums all = warp_scan(warp_sums[lane]);
+  total = from_lane(all, 31);
+  const Sums upto = from_lane(all, max(warp - 1, 0));
+  const Sums before = warp == 0 ? Sums{0, 0, 0} : upto;
   return Sums{before.rows + inc.rows - mine.rows, before.take + inc.take - mine.take,
               before.give + inc.give - mine.give};
 }
@@ -72,34 +81,31 @@ __device__ __forceinline__ SeqPlan seq_plan(const PlanArgs& a, int b, int32_t* f
   s.need = s.bad ? 0 : (s.len + s.count + 63) / 64;
   return s;
 }
+__device__ __forceinline__ Sums sums_of(const SeqPlan& s) {
+  if (s.bad) return Sums{0, 0, 0};
+  return Sums{s.count, max(s.need - s.held, 0), max(s.held - s.need, 0)};
+}
 
-// One new row: its sequence by a search in row_start, then slot, position and mask.
-__device__ __forceinline__ void write_row(const PlanArgs& a, int n) {
-  const int total = a.row_start[a.batch];
-  if (n >= total) {                             // rows behind the last sequence
-    a.slots[n] = -1;
-    a.positions[n] = 0;
-    if (a.seq_ids) a.seq_ids[n] = -1;
-    if (a.mask)
-      for (int w = 0; w < a.mask_words; ++w) a.mask[(size_t)n * a.mask_words + w] = 0;
-    return;
-  }
-  int lo = 0, hi = a.batch - 1;                 // the last sequence that starts at or before n
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.row_start[mid] <= n) lo = mid; else hi = mid - 1;
-  }
-  const int b = lo, s0 = a.row_start[b], i = n - s0;
-  const int len = a.kv_lens[b] - (a.row_start[b + 1] - s0);
-  const int row = len + i;
-  const int page = a.block_table[(size_t)b * a.max_pages + (row >> 6)];
+// A row behind the last sequence.
+__device__ __forceinline__ void write_padding(const PlanArgs& a, int n) {
+  a.slots[n] = -1;
+  a.positions[n] = 0;
+  if (a.seq_ids) a.seq_ids[n] = -1;
+  if (a.mask)
+    for (int w = 0; w < a.mask_words; ++w) a.mask[(size_t)n * a.mask_words + w] = 0;
+}
+
+// Slot, position and mask of node i of sequence b (new row n), whose page is
+// `page`; par: the parents of the sequence's nodes (NULL: a chain).
+__device__ __forceinline__ void write_row(const PlanArgs& a, int n, int b, int i, int len, int page,
+                                          const int32_t* par) {
   const bool ok = page >= 0 && page < a.num_pages;
   if (!ok) flag_error(a.err, MLA_DEVERR_PAGE);
-  a.slots[n] = ok ? page * 64 + (row & 63) : -1;
+  a.slots[n] = ok ? page * 64 + ((len + i) & 63) : -1;
   if (a.seq_ids) a.seq_ids[n] = b;
   int depth = i;
-  if (a.parents) {
-    // up the tree: parents come before their children, so the walk ends
+  if (par) {
+    // up the tree: a parent comes before its children, so the walk ends
     depth = 0;
     uint64_t word = 1ull << (i & 63);
     int w = i >> 6;
@@ -108,7 +114,7 @@ __device__ __forceinline__ void write_row(const PlanArgs& a, int n) {
       for (int v = w + 1; v < a.mask_words; ++v) mask[v] = 0;
     int at = i;
     while (true) {
-      const int up = a.parents[s0 + at];
+      const int up = par[at];
       if (up < 0) break;
       if (up >= at) {                           // not a tree in topological order: taken as a root
         flag_error(a.err, MLA_DEVERR_POSITION);
@@ -137,22 +143,41 @@ __device__ __forceinline__ void write_row(const PlanArgs& a, int n) {
   a.positions[n] = len + depth;
 }
 
+// The last sequence that starts at or before row n (start ascends, start[0] <= n).
+__device__ __forceinline__ int find_seq(const int* start, int batch, int n) {
+  int lo = 0, hi = batch - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (start[mid] <= n) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// inline_rows: rows this CTA writes itself (at most kInlineRows, and only
+// where the batch is one round).  parents of those rows wait in shared memory
+// by then, and a new page is read straight from the free list, so that no
+// load waits for a store of this kernel.
 __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanArgs a, int inline_rows) {
   __shared__ Sums warp_sums[kWarps];
-  __shared__ int s_take[kThreads], s_give[kThreads], s_held[kThreads], s_need[kThreads];
+  __shared__ int s_take[kThreads], s_give[kThreads], s_held[kThreads], s_need[kThreads], s_len[kThreads];
+  __shared__ int s_start[kThreads + 1];
+  __shared__ int s_par[kInlineRows];
   griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (a.parents)
+    for (int n = tid; n < inline_rows; n += kThreads) s_par[n] = a.parents[n];
   int32_t flags = 0;
   // ---- totals: does the step fit?
+  SeqPlan own{0, 0, 0, 0, true};                // this thread's sequence, where the batch is one round
   Sums mine{0, 0, 0};
+  const int free_in = *a.free_count_in;
   for (int b = tid; b < a.batch; b += kThreads) {
-    const SeqPlan s = seq_plan(a, b, &flags);
-    mine = add(mine, Sums{s.bad ? 0 : s.count, max(s.need - s.held, 0), s.bad ? 0 : max(s.held - s.need, 0)});
+    own = seq_plan(a, b, &flags);
+    mine = add(mine, sums_of(own));
   }
   Sums total;
-  const int free_in = *a.free_count_in;
-  block_scan(mine, warp_sums, total);
+  const Sums first = block_scan(mine, warp_sums, total);
   if (free_in < 0 || free_in > a.num_pages || (long long)free_in + total.give > a.num_pages)
     flags |= MLA_DEVERR_POSITION;
   else if (total.take > free_in + total.give || total.rows > a.max_rows)
@@ -160,26 +185,46 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanArgs a, int inlin
   flags = __reduce_or_sync(0xffffffffu, flags);
   if (lane == 0 && flags) flag_error(a.err, flags);
   const bool fits = !__syncthreads_or(flags != 0);
+  if (!fits) {
+    for (int b = tid; b < a.batch; b += kThreads) {
+      a.row_start[b] = 0;
+      a.kv_lens[b] = a.seq_lens[b];
+      a.held_out[b] = a.held_in[b];
+    }
+    if (tid == 0) {
+      a.row_start[a.batch] = 0;
+      *a.free_count_out = free_in;
+    }
+    for (int n = tid; n < inline_rows; n += kThreads) write_padding(a, n);
+    return;
+  }
   // ---- state: sequences in rounds of 1024, pages given back before any is taken
+  const bool one_round = a.batch <= kThreads;
   const int top = free_in + total.give;
-  for (int pass = 0; pass < 2; ++pass) {        // 0: give back and row offsets, 1: take
+  for (int pass = total.give > 0 ? 0 : 1; pass < 2; ++pass) {     // 0: give back, 1: take
     Sums carry{0, 0, 0};
     for (int base = 0; base < a.batch; base += kThreads) {
       const int b = base + tid;
       int32_t ignored = 0;
-      SeqPlan s{0, 0, 0, 0, true};
-      if (b < a.batch && fits) s = seq_plan(a, b, &ignored);
-      const Sums v{s.bad ? 0 : s.count, s.bad ? 0 : max(s.need - s.held, 0), s.bad ? 0 : max(s.held - s.need, 0)};
-      Sums round;
-      const Sums ex = add(carry, block_scan(v, warp_sums, round));
-      carry = add(carry, round);
+      Sums ex = first;
+      SeqPlan s = own;
+      if (!one_round) {
+        s = SeqPlan{0, 0, 0, 0, true};
+        if (b < a.batch) s = seq_plan(a, b, &ignored);
+        Sums round;
+        ex = add(carry, block_scan(sums_of(s), warp_sums, round));
+        carry = add(carry, round);
+      }
       s_take[tid] = ex.take;
       s_give[tid] = ex.give;
-      s_held[tid] = s.bad ? 0 : s.held;
-      s_need[tid] = s.bad ? 0 : s.need;
-      if (pass == 0 && b < a.batch) {
+      s_held[tid] = s.held;
+      s_need[tid] = s.need;
+      s_len[tid] = s.len;
+      s_start[tid] = (int)ex.rows;
+      if (pass == 1 && b < a.batch) {
         a.row_start[b] = (int)ex.rows;
-        a.kv_lens[b] = fits ? s.len + s.count : a.seq_lens[b];
+        a.kv_lens[b] = s.len + s.count;
+        a.held_out[b] = s.need;                 // may be held_in: this round has read its own
       }
       __syncthreads();
       // a warp per sequence, a lane per page
@@ -195,33 +240,66 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanArgs a, int inlin
           for (int k = held + lane; k < need; k += 32) row[k] = a.free_pages[top - 1 - (s_take[q] + k - held)];
         }
       }
-      __syncthreads();
-      // held_out may be held_in: a round is written once nothing reads it any more
-      if (pass == 1 && b < a.batch) a.held_out[b] = fits ? s.need : a.held_in[b];
+      if (!one_round || pass == 0) __syncthreads();
     }
   }
   if (tid == 0) {
-    a.row_start[a.batch] = fits ? (int)total.rows : 0;
-    *a.free_count_out = fits ? top - total.take : free_in;
+    a.row_start[a.batch] = (int)total.rows;
+    *a.free_count_out = top - total.take;
   }
-  __syncthreads();
-  for (int n = tid; n < inline_rows; n += kThreads) write_row(a, n);
+  for (int n = tid; n < inline_rows; n += kThreads) {
+    if (n >= total.rows) {
+      write_padding(a, n);
+      continue;
+    }
+    const int b = find_seq(s_start, a.batch, n), s0 = s_start[b], i = n - s0, len = s_len[b];
+    const int k = (len + i) >> 6, held = s_held[b];
+    const int page = k < held ? a.block_table[(size_t)b * a.max_pages + k]
+                              : a.free_pages[top - 1 - (s_take[b] + k - held)];
+    write_row(a, n, b, i, len, page, a.parents ? s_par + s0 : nullptr);
+  }
 }
+
+// Many rows: a thread per four consecutive rows, found by one search.
+constexpr int kRowsPerThread = 4;
 
 __global__ void __launch_bounds__(256) plan_rows_kernel(PlanArgs a) {
   griddep_wait();
   griddep_launch_dependents();
-  const int n = blockIdx.x * blockDim.x + threadIdx.x;
-  if (n < a.max_rows) write_row(a, n);
+  const int n0 = (blockIdx.x * blockDim.x + threadIdx.x) * kRowsPerThread;
+  const int total = a.row_start[a.batch];
+  const int end = min(a.max_rows, n0 + kRowsPerThread);
+  if (n0 >= end) return;
+  int b = -1, s0 = 0, s1 = 0, len = 0, k = -1, page = -1;
+  for (int n = n0; n < end; ++n) {
+    if (n >= total) {
+      write_padding(a, n);
+      continue;
+    }
+    if (n >= s1) {                              // the first row, or past its sequence's end
+      b = find_seq(a.row_start, a.batch, n);
+      s0 = a.row_start[b];
+      s1 = a.row_start[b + 1];
+      len = a.kv_lens[b] - (s1 - s0);
+      k = -1;
+    }
+    const int i = n - s0;
+    if ((len + i) >> 6 != k) {
+      k = (len + i) >> 6;
+      page = a.block_table[(size_t)b * a.max_pages + k];
+    }
+    write_row(a, n, b, i, len, page, a.parents ? a.parents + s0 : nullptr);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_step_plan(const PlanArgs& a, cudaStream_t st) {
-  const bool in_one = a.max_rows <= kInlineRows;
+  const bool in_one = a.max_rows <= kInlineRows && a.batch <= kThreads;
   cudaError_t e = launch_dependent(plan_kernel, dim3(1), dim3(kThreads), 0, st, a, in_one ? a.max_rows : 0);
-  if (e != cudaSuccess || in_one) return e;
-  return launch_dependent(plan_rows_kernel, dim3((unsigned)((a.max_rows + 255) / 256)), dim3(256), 0, st, a);
+  if (e != cudaSuccess || in_one || a.max_rows == 0) return e;
+  const unsigned per_cta = 256 * kRowsPerThread;
+  return launch_dependent(plan_rows_kernel, dim3(((unsigned)a.max_rows + per_cta - 1) / per_cta), dim3(256), 0, st, a);
 }
 
 }  // namespace mla
