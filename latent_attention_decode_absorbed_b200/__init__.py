@@ -77,6 +77,20 @@ def lib():
     return _lib
 
 
+_marshal = None
+
+
+def native():
+    """The module that marshals the drafted-step calls (over the library that
+    lib() loads).  Raises if it has not been built."""
+    global _marshal
+    if _marshal is None:
+        lib()
+        from . import _native
+        _marshal = _native
+    return _marshal
+
+
 def status_string(status: int) -> str:
     return lib().mla_status_string(int(status)).decode()
 
@@ -189,20 +203,22 @@ def mla_step_plan(seq_lens, new_counts, parents, batch, max_rows, mask_words, he
     """Pages, block table, row offsets, slots, positions and ancestor masks of a
     step, from device lengths, row counts and drafted trees (parents, seq_ids
     and tree_mask may be None); tree_mask: int64 [max_rows, mask_words]."""
-    _check("mla_step_plan", lib().mla_step_plan(
-        _ptr(seq_lens), _ptr(new_counts), _ptr(parents), int(batch), int(max_rows), int(mask_words), _ptr(held_in),
-        _ptr(held_out), _ptr(free_pages), _ptr(free_count_in), _ptr(free_count_out), _ptr(block_table),
-        int(max_pages_per_seq), int(page_size), int(num_pages), _ptr(row_start), _ptr(kv_lens), _ptr(seq_ids),
-        _ptr(positions), _ptr(slots), _ptr(tree_mask), _ptr(err_word), _stream(stream)))
+    status = native().step_plan(seq_lens, new_counts, parents, batch, max_rows, mask_words, held_in, held_out,
+                                free_pages, free_count_in, free_count_out, block_table, max_pages_per_seq, page_size,
+                                num_pages, row_start, kv_lens, seq_ids, positions, slots, tree_mask, err_word,
+                                _stream(stream))
+    if status:
+        _check("mla_step_plan", status)
 
 
 def mla_cache_append_slots(kv_a, kv_dtype, n_new, slots, positions, norm_gain, eps, rope_cos, rope_sin,
                            rope_max_pos, cache, cache_scale, cache_dtype, num_pages, err_word=None, stream=None):
     """mla_cache_append's rows at given slots (-1: skipped), rotated to given positions."""
-    _check("mla_cache_append_slots", lib().mla_cache_append_slots(
-        _ptr(kv_a), int(kv_dtype), int(n_new), _ptr(slots), _ptr(positions), _ptr(norm_gain), float(eps),
-        _ptr(rope_cos), _ptr(rope_sin), int(rope_max_pos), _ptr(cache), _ptr(cache_scale), int(cache_dtype),
-        int(num_pages), _ptr(err_word), _stream(stream)))
+    status = native().cache_append_slots(kv_a, kv_dtype, n_new, slots, positions, norm_gain, eps, rope_cos, rope_sin,
+                                         rope_max_pos, cache, cache_scale, cache_dtype, num_pages, err_word,
+                                         _stream(stream))
+    if status:
+        _check("mla_cache_append_slots", status)
 
 
 def mla_decode_tree_workspace_bytes(cache_dtype: int, max_rows: int, n_heads: int) -> int:
@@ -215,11 +231,12 @@ def mla_decode_tree(q_abs, q_dtype, cache, cache_scale, cache_dtype, num_pages, 
                     workspace, o_lat, o_dtype, lse_out=None, err_word=None, stream=None):
     """Attention and merge of a ragged number of drafted tokens per sequence, each
     seeing its prefix and the drafted rows of its mask (None: a chain)."""
-    _check("mla_decode_tree", lib().mla_decode_tree(
-        _ptr(q_abs), int(q_dtype), _ptr(cache), _ptr(cache_scale), int(cache_dtype), int(num_pages),
-        _ptr(block_table), int(max_pages_per_seq), int(page_size), _ptr(kv_lens), _ptr(row_start), int(batch),
-        int(max_rows), int(n_heads), _ptr(tree_mask), int(mask_words), float(softmax_scale), _ptr(workspace),
-        _ptr(o_lat), int(o_dtype), _ptr(lse_out), _ptr(err_word), _stream(stream)))
+    status = native().decode_tree(q_abs, q_dtype, cache, cache_scale, cache_dtype, num_pages, block_table,
+                                  max_pages_per_seq, page_size, kv_lens, row_start, batch, max_rows, n_heads,
+                                  tree_mask, mask_words, softmax_scale, workspace, o_lat, o_dtype, lse_out, err_word,
+                                  _stream(stream))
+    if status:
+        _check("mla_decode_tree", status)
 
 
 def mla_cache_commit(kv_lens, row_start, batch, max_rows, accept_counts, accept_nodes, block_table,
@@ -227,10 +244,11 @@ def mla_cache_commit(kv_lens, row_start, batch, max_rows, accept_counts, accept_
                      err_word=None, stream=None):
     """Move each sequence's accepted path of drafted rows to the front of its
     drafted rows; seq_lens_out: the lengths after it."""
-    _check("mla_cache_commit", lib().mla_cache_commit(
-        _ptr(kv_lens), _ptr(row_start), int(batch), int(max_rows), _ptr(accept_counts), _ptr(accept_nodes),
-        _ptr(block_table), int(max_pages_per_seq), int(page_size), _ptr(cache), _ptr(cache_scale), int(cache_dtype),
-        int(num_pages), _ptr(seq_lens_out), _ptr(err_word), _stream(stream)))
+    status = native().cache_commit(kv_lens, row_start, batch, max_rows, accept_counts, accept_nodes, block_table,
+                                   max_pages_per_seq, page_size, cache, cache_scale, cache_dtype, num_pages,
+                                   seq_lens_out, err_word, _stream(stream))
+    if status:
+        _check("mla_cache_commit", status)
 
 
 def mla_combine(o_part, lse_part, rows, n_heads, num_splits, o_lat, o_dtype, lse_out=None, stream=None):

@@ -2,8 +2,9 @@
 
     python -m latent_attention_decode_absorbed_b200.build [--force] [-v]
 
-Objects go to ``_build/`` at the repository root; the shared library lands
-next to this file so it travels with the source tree.
+Objects go to ``_build/`` at the repository root; the shared library and the
+Python module linked against it land next to this file so they travel with
+the source tree.
 """
 from __future__ import annotations
 
@@ -14,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmla.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_native.so")     # the Python module that marshals the drafted-step calls
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -72,7 +76,25 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    _build_binding(force, verbose)
     return LIB
+
+
+def _build_binding(force: bool, verbose: bool):
+    """The Python module over libmla.so (found next to it at load time)."""
+    newest = max(os.path.getmtime(f) for f in [BINDING_SRC, os.path.join(INCLUDE, "mla.h")])
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return
+    tmp = BINDING + ".tmp"
+    cmd = [nvcc(), "-O2", "-std=c++17", "-Xcompiler", "-fPIC", "-shared", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], "-o", tmp, BINDING_SRC, "-L", PKG, "-l:libmla.so",
+           "-Xlinker", "-rpath=$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"binding build failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 if __name__ == "__main__":

@@ -795,11 +795,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
+__device__ __forceinline__ void store4(float* dst, float4 v, float f) {
+  *reinterpret_cast<float4*>(dst) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* dst, float4 v, float f) {
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(v.x * f, v.y * f), pack_bf16(v.z * f, v.w * f));
+}
+
 // Joins the partials of the row tiles that crossed a pair's border: pair p's
 // last segment (slot 2 p + 1) and the first segments (slot 2 q) of the pairs
-// that follow it.  CTA (p, y): rows 4 y .. 4 y + 3 of pair p's row tile, 128
-// threads x 4 channels per row.  Memory-bound: each partial is read once.
-constexpr int kMergeRows = 4;
+// that follow it.  CTA (p, y): rows 2 y and 2 y + 1 of pair p's row tile, 128
+// threads x 4 channels per row.  Each partial is read once, and a call of few
+// tiles is bound by latency: a descriptor, then all parts' loads at once (the
+// weights are worked out while the values are on their way).
+constexpr int kMergeRows = 2;
+constexpr int kMergeBatch = 16;
 
 template <typename OT>
 __global__ void __launch_bounds__(128 * kMergeRows) tree_merge_kernel(const float* __restrict__ part_o,
@@ -812,42 +822,49 @@ __global__ void __launch_bounds__(128 * kMergeRows) tree_merge_kernel(const floa
   const int pair = blockIdx.x;
   const TreeDesc d = desc[pair];
   const int j = blockIdx.y * kMergeRows + (threadIdx.x >> 7);
-  const int c = threadIdx.x & 127;
+  const int c = threadIdx.x & 127, lane = threadIdx.x & 31;
   if (d.follow == 0 || j >= d.rows) return;
+  const int parts = d.follow + 1;
   auto slot = [&](int k) { return k == 0 ? 2 * pair + 1 : 2 * (pair + k); };
+  // lane k of each warp holds the log-normalisers of parts k, k + 32, ... (at most 96 pairs)
+  float ls[3];
   float mx = -INFINITY;
-  for (int k = 0; k <= d.follow; ++k) mx = fmaxf(mx, part_lse[slot(k) * kM + j]);
+#pragma unroll
+  for (int t = 0; t < 3; ++t) {
+    const int k = lane + 32 * t;
+    ls[t] = k < parts ? part_lse[slot(k) * kM + j] : -INFINITY;
+  }
   float sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (mx != -INFINITY) {
-    for (int k0 = 0; k0 <= d.follow; k0 += 8) {   // eight parts' loads in flight
-      float w[8];
-      float4 v[8];
+  for (int k0 = 0; k0 < parts; k0 += kMergeBatch) {
+    float4 v[kMergeBatch];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const bool in = k0 + k <= d.follow;
-        const int sl = slot(in ? k0 + k : 0);
-        w[k] = in ? expf(part_lse[sl * kM + j] - mx) : 0.f;
-        v[k] = in ? reinterpret_cast<const float4*>(part_o + ((size_t)sl * kM + j) * MLA_D_C)[c]
-                  : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
+    for (int k = 0; k < kMergeBatch; ++k)
+      v[k] = k0 + k < parts ? reinterpret_cast<const float4*>(part_o + ((size_t)slot(k0 + k) * kM + j) * MLA_D_C)[c]
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+    if (k0 == 0) {
+      mx = warp_max(fmaxf(fmaxf(ls[0], ls[1]), ls[2]));
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        sum += w[k];
-        acc.x = fmaf(w[k], v[k].x, acc.x);
-        acc.y = fmaf(w[k], v[k].y, acc.y);
-        acc.z = fmaf(w[k], v[k].z, acc.z);
-        acc.w = fmaf(w[k], v[k].w, acc.w);
+      for (int t = 0; t < 3; ++t) {
+        ls[t] = mx == -INFINITY ? 0.f : expf(ls[t] - mx);
+        sum += ls[t];
       }
+      sum = warp_sum(sum);
+    }
+#pragma unroll
+    for (int k = 0; k < kMergeBatch; ++k) {
+      const int t = (k0 + k) >> 5;
+      const float w = __shfl_sync(0xffffffffu, t == 0 ? ls[0] : t == 1 ? ls[1] : ls[2], (k0 + k) & 31);
+      acc.x = fmaf(w, v[k].x, acc.x);
+      acc.y = fmaf(w, v[k].y, acc.y);
+      acc.z = fmaf(w, v[k].z, acc.z);
+      acc.w = fmaf(w, v[k].w, acc.w);
     }
   }
   const float inv = sum > 0.f ? 1.0f / sum : 0.f;
   const size_t row = (size_t)d.row0 + j;
   OT* dst = o_lat + row * MLA_D_C + 4 * c;
-  dst[0] = from_f32<OT>(acc.x * inv);
-  dst[1] = from_f32<OT>(acc.y * inv);
-  dst[2] = from_f32<OT>(acc.z * inv);
-  dst[3] = from_f32<OT>(acc.w * inv);
+  store4(dst, acc, inv);
   if (lse_out && c == 0) lse_out[row] = sum > 0.f ? mx + logf(sum) : -INFINITY;
 }
 
@@ -948,26 +965,26 @@ __global__ void __launch_bounds__(32 * kSimtWarps) decode_tree_simt_kernel(const
   griddep_wait();
   griddep_launch_dependents();
   const int split = blockIdx.x, n = blockIdx.z;
-  SeqInfo s;
-  const int b = seq_of(p, n, s);
-  if (b < 0) {
-    if (threadIdx.x == 0 && n >= p.row_start[0] && n < p.row_start[p.batch]) flag_error(p.err, MLA_DEVERR_POSITION);
-    return;
-  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h0 = blockIdx.y * kSimtHeads + 2 * warp;
   const int heads = min(max(p.n_heads - h0, 0), 2);      // of this warp
-  const int node = n - s.start, prefix = s.L - s.n;
-  const int groups = (s.L + kSimtGroup - 1) / kSimtGroup;
-  const int lo = (int)((long long)groups * split / splits) * kSimtGroup;
-  const int hi = min((int)((long long)groups * (split + 1) / splits) * kSimtGroup, s.L);
-  const uint64_t* mask = p.tree_mask ? p.tree_mask + (size_t)n * p.mask_words : nullptr;
   const size_t vec = (size_t)n * p.n_heads + h0;
   float q[2][18];
 #pragma unroll
   for (int e = 0; e < 2; ++e)
 #pragma unroll
     for (int k = 0; k < 18; ++k) q[e][k] = e < heads ? q_abs[(vec + e) * MLA_D_ROW + lane + 32 * k] : 0.f;
+  SeqInfo s;
+  const int b = seq_of(p, n, s);
+  if (b < 0) {
+    if (threadIdx.x == 0 && n >= p.row_start[0] && n < p.row_start[p.batch]) flag_error(p.err, MLA_DEVERR_POSITION);
+    return;
+  }
+  const int node = n - s.start, prefix = s.L - s.n;
+  const int groups = (s.L + kSimtGroup - 1) / kSimtGroup;
+  const int lo = (int)((long long)groups * split / splits) * kSimtGroup;
+  const int hi = min((int)((long long)groups * (split + 1) / splits) * kSimtGroup, s.L);
+  const uint64_t* mask = p.tree_mask ? p.tree_mask + (size_t)n * p.mask_words : nullptr;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   float o[2][16];
 #pragma unroll
@@ -1054,48 +1071,51 @@ __global__ void __launch_bounds__(32 * kSimtWarps) decode_tree_simt_kernel(const
   }
 }
 
+// CTA = one (node, head) vector; four groups of 128 threads take every fourth
+// split, so that all splits' loads are in flight at once.
 template <typename OT>
-__global__ void __launch_bounds__(128) tree_merge_f32_kernel(TreeParams p, int splits) {
+__global__ void __launch_bounds__(512) tree_merge_f32_kernel(TreeParams p, int splits) {
+  __shared__ float4 sums[4][128];
   griddep_wait();
   griddep_launch_dependents();
   const size_t vec = blockIdx.x;
-  SeqInfo s;
-  if (seq_of(p, (int)(vec / p.n_heads), s) < 0) return;
+  const int lane = threadIdx.x & 31, grp = threadIdx.x >> 7, c = threadIdx.x & 127;
+  // every load is independent of the others: the row's validity is looked at before the store only
   const float* lp = p.part_lse + vec * splits;
-  const int lane = threadIdx.x & 31;
-  const float4* op = reinterpret_cast<const float4*>(p.part_o + vec * splits * MLA_D_C) + threadIdx.x;
-  float mx = -INFINITY;
-  for (int k = lane; k < splits; k += 32) mx = fmaxf(mx, lp[k]);
-  mx = warp_max(mx);
-  float sum = 0.f;
+  const float4* op = reinterpret_cast<const float4*>(p.part_o + vec * splits * MLA_D_C) + c;
+  float l0 = lane < splits ? lp[lane] : -INFINITY, l1 = lane + 32 < splits ? lp[lane + 32] : -INFINITY;
+  float4 v[16];                              // at most 64 splits
+#pragma unroll
+  for (int k = 0; k < 16; ++k)
+    v[k] = grp + 4 * k < splits ? op[(size_t)(grp + 4 * k) * (MLA_D_C / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+  SeqInfo s;
+  const bool valid = seq_of(p, (int)(vec / p.n_heads), s) >= 0;
+  const float mx = warp_max(fmaxf(l0, l1));
+  l0 = mx == -INFINITY ? 0.f : expf(l0 - mx);
+  l1 = mx == -INFINITY ? 0.f : expf(l1 - mx);
+  const float sum = warp_sum(l0 + l1);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (mx != -INFINITY) {
-    for (int k0 = 0; k0 < splits; k0 += 8) {     // eight parts' loads in flight
-      float w[8];
-      float4 v[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int at = min(k0 + k, splits - 1);
-        w[k] = k0 + k < splits ? expf(lp[at] - mx) : 0.f;
-        v[k] = op[(size_t)at * (MLA_D_C / 4)];
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        sum += w[k];
-        acc.x = fmaf(w[k], v[k].x, acc.x);
-        acc.y = fmaf(w[k], v[k].y, acc.y);
-        acc.z = fmaf(w[k], v[k].z, acc.z);
-        acc.w = fmaf(w[k], v[k].w, acc.w);
-      }
-    }
+  for (int k = 0; k < 16; ++k) {
+    const float w = __shfl_sync(0xffffffffu, k < 8 ? l0 : l1, (grp + 4 * k) & 31);
+    acc.x = fmaf(w, v[k].x, acc.x);
+    acc.y = fmaf(w, v[k].y, acc.y);
+    acc.z = fmaf(w, v[k].z, acc.z);
+    acc.w = fmaf(w, v[k].w, acc.w);
   }
-  const float inv = sum > 0.f ? 1.0f / sum : 0.f;
-  OT* dst = reinterpret_cast<OT*>(p.o_lat) + vec * MLA_D_C + 4 * threadIdx.x;
-  dst[0] = from_f32<OT>(acc.x * inv);
-  dst[1] = from_f32<OT>(acc.y * inv);
-  dst[2] = from_f32<OT>(acc.z * inv);
-  dst[3] = from_f32<OT>(acc.w * inv);
-  if (p.lse && threadIdx.x == 0) p.lse[vec] = sum > 0.f ? mx + logf(sum) : -INFINITY;
+  sums[grp][c] = acc;
+  __syncthreads();
+  if (grp || !valid) return;
+#pragma unroll
+  for (int g = 1; g < 4; ++g) {
+    const float4 x = sums[g][c];
+    acc.x += x.x;
+    acc.y += x.y;
+    acc.z += x.z;
+    acc.w += x.w;
+  }
+  store4(reinterpret_cast<OT*>(p.o_lat) + vec * MLA_D_C + 4 * c, acc, sum > 0.f ? 1.0f / sum : 0.f);
+  if (p.lse && c == 0) p.lse[vec] = sum > 0.f ? mx + logf(sum) : -INFINITY;
 }
 
 // ------------------------------------------------------------------ host side
@@ -1226,8 +1246,8 @@ cudaError_t launch_decode_tree(const TreeArgs& a, cudaStream_t st) {
                          static_cast<const float*>(a.q_abs), static_cast<const float*>(a.cache), p, splits);
     if (e != cudaSuccess) return e;
     const dim3 mg((unsigned)((long long)a.rows * a.n_heads));
-    if (a.o_dtype == MLA_F32) return launch_dependent(tree_merge_f32_kernel<float>, mg, dim3(128), 0, st, p, splits);
-    return launch_dependent(tree_merge_f32_kernel<__nv_bfloat16>, mg, dim3(128), 0, st, p, splits);
+    if (a.o_dtype == MLA_F32) return launch_dependent(tree_merge_f32_kernel<float>, mg, dim3(512), 0, st, p, splits);
+    return launch_dependent(tree_merge_f32_kernel<__nv_bfloat16>, mg, dim3(512), 0, st, p, splits);
   }
   p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
   p.desc = reinterpret_cast<TreeDesc*>(ws + w.desc);

@@ -25,11 +25,14 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kInlineRows = 4096;     // rows that the state's CTA writes itself
+constexpr int kSeqsAtOnce = 4;
 
-struct Sums { long long rows; int take, give; };
+// rows saturates at kManyRows, so that no sum of counts wraps
+struct Sums { unsigned rows; int take, give; };
+constexpr unsigned kManyRows = 0x7fffffffu;
 
 __device__ __forceinline__ Sums add(const Sums& a, const Sums& b) {
-  return Sums{a.rows + b.rows, a.take + b.take, a.give + b.give};
+  return Sums{min(a.rows + b.rows, kManyRows), a.take + b.take, a.give + b.give};
 }
 
 __device__ __forceinline__ Sums warp_scan(Sums v) {   // inclusive
@@ -42,24 +45,26 @@ __device__ __forceinline__ Sums warp_scan(Sums v) {   // inclusive
   }
   return v;
 }
-__device__ __forceinline__ Sums from_lane(const Sums& v, int lane) {
-  return Sums{__shfl_sync(0xffffffffu, v.rows, lane), __shfl_sync(0xffffffffu, v.take, lane),
-              __shfl_sync(0xffffffffu, v.give, lane)};
-}
 
-// Exclusive prefix of each thread's sums within the CTA, and the CTA's total.
-// Every warp scans the warps' sums for itself: one barrier fewer than a
-// second level in one warp, and no loop over 32 of them.
-__device__ __forceinline__ Sums block_scan(const Sums& mine, Sums* warp_sums, Sums& total) {
+// Exclusive prefix of each thread's sums within the CTA, and the CTA's total;
+// only the first `live` threads' sums are not zero.  Shuffles bound this (one
+// warp's per cycle), so warps without a sum leave the scan out and one warp
+// scans the warps' sums.
+__device__ __forceinline__ Sums block_scan(const Sums& mine, int live, Sums* warp_sums, Sums& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Sums inc = warp_scan(mine);
+  Sums inc{0, 0, 0};
+  if (32 * warp < live) inc = warp_scan(mine);
   __syncthreads();                       // the previous use of warp_sums is over
   if (lane == 31) warp_sums[warp] = inc;
   __syncthreads();
-  const Sums all = warp_scan(warp_sums[lane]);
-  total = from_lane(all, 31);
-  const Sums upto = from_lane(all, max(warp - 1, 0));
-  const Sums before = warp == 0 ? Sums{0, 0, 0} : upto;
+  if (warp == 0) {
+    const Sums w = warp_sums[lane], upto = warp_scan(w);
+    warp_sums[lane] = Sums{upto.rows - w.rows, upto.take - w.take, upto.give - w.give};
+    if (lane == 31) warp_sums[kWarps] = upto;
+  }
+  __syncthreads();
+  total = warp_sums[kWarps];
+  const Sums before = warp_sums[warp];
   return Sums{before.rows + inc.rows - mine.rows, before.take + inc.take - mine.take,
               before.give + inc.give - mine.give};
 }
@@ -83,7 +88,7 @@ __device__ __forceinline__ SeqPlan seq_plan(const PlanArgs& a, int b, int32_t* f
 }
 __device__ __forceinline__ Sums sums_of(const SeqPlan& s) {
   if (s.bad) return Sums{0, 0, 0};
-  return Sums{s.count, max(s.need - s.held, 0), max(s.held - s.need, 0)};
+  return Sums{(unsigned)s.count, max(s.need - s.held, 0), max(s.held - s.need, 0)};
 }
 
 // A row behind the last sequence.
@@ -158,7 +163,7 @@ __device__ __forceinline__ int find_seq(const int* start, int batch, int n) {
 // by then, and a new page is read straight from the free list, so that no
 // load waits for a store of this kernel.
 __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanArgs a, int inline_rows) {
-  __shared__ Sums warp_sums[kWarps];
+  __shared__ Sums warp_sums[kWarps + 1];
   __shared__ int s_take[kThreads], s_give[kThreads], s_held[kThreads], s_need[kThreads], s_len[kThreads];
   __shared__ int s_start[kThreads + 1];
   __shared__ int s_par[kInlineRows];
@@ -177,10 +182,10 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanArgs a, int inlin
     mine = add(mine, sums_of(own));
   }
   Sums total;
-  const Sums first = block_scan(mine, warp_sums, total);
+  const Sums first = block_scan(mine, min(a.batch, kThreads), warp_sums, total);
   if (free_in < 0 || free_in > a.num_pages || (long long)free_in + total.give > a.num_pages)
     flags |= MLA_DEVERR_POSITION;
-  else if (total.take > free_in + total.give || total.rows > a.max_rows)
+  else if (total.take > free_in + total.give || total.rows > (unsigned)a.max_rows)
     flags |= MLA_DEVERR_CAPACITY;
   flags = __reduce_or_sync(0xffffffffu, flags);
   if (lane == 0 && flags) flag_error(a.err, flags);
@@ -212,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanArgs a, int inlin
         s = SeqPlan{0, 0, 0, 0, true};
         if (b < a.batch) s = seq_plan(a, b, &ignored);
         Sums round;
-        ex = add(carry, block_scan(sums_of(s), warp_sums, round));
+        ex = add(carry, block_scan(sums_of(s), min(a.batch - base, kThreads), warp_sums, round));
         carry = add(carry, round);
       }
       s_take[tid] = ex.take;
@@ -227,17 +232,42 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanArgs a, int inlin
         a.held_out[b] = s.need;                 // may be held_in: this round has read its own
       }
       __syncthreads();
-      // a warp per sequence, a lane per page
-      for (int q = warp; q < kThreads && base + q < a.batch; q += kWarps) {
+      // a warp per sequence, a lane per page: the first 64 pages of four
+      // sequences are loaded before any is stored
+      const int seqs = min(kThreads, a.batch - base);
+      // the k-th page that sequence q gives back (pass 0) or takes (pass 1)
+      auto moves = [&](int q, int k) {
+        return q < seqs && k < (pass == 0 ? s_held[q] - s_need[q] : s_need[q] - s_held[q]);
+      };
+      auto load_page = [&](int q, int k) -> int {
+        if (!moves(q, k)) return -1;
+        return pass == 0 ? a.block_table[(size_t)(base + q) * a.max_pages + s_need[q] + k]
+                         : a.free_pages[top - 1 - (s_take[q] + k)];
+      };
+      auto store_page = [&](int q, int k, int page) {
+        if (!moves(q, k)) return;
         int32_t* row = a.block_table + (size_t)(base + q) * a.max_pages;
-        const int held = s_held[q], need = s_need[q];
         if (pass == 0) {
-          for (int k = need + lane; k < held; k += 32) {
-            a.free_pages[free_in + s_give[q] + k - need] = row[k];
-            row[k] = -1;
-          }
+          a.free_pages[free_in + s_give[q] + k] = page;
+          row[s_need[q] + k] = -1;
         } else {
-          for (int k = held + lane; k < need; k += 32) row[k] = a.free_pages[top - 1 - (s_take[q] + k - held)];
+          row[s_held[q] + k] = page;
+        }
+      };
+      for (int q0 = warp; q0 < seqs; q0 += kSeqsAtOnce * kWarps) {
+        int page[kSeqsAtOnce][2];
+#pragma unroll
+        for (int u = 0; u < kSeqsAtOnce; ++u)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) page[u][t] = load_page(q0 + u * kWarps, lane + 32 * t);
+#pragma unroll
+        for (int u = 0; u < kSeqsAtOnce; ++u) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) store_page(q0 + u * kWarps, lane + 32 * t, page[u][t]);
+          const int q = q0 + u * kWarps;
+          const int count = q < seqs ? abs(s_need[q] - s_held[q]) : 0;
+          for (int k = 64 + lane; k < count; k += 32)
+            store_page(q, k, load_page(q, k));
         }
       }
       if (!one_round || pass == 0) __syncthreads();
@@ -248,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanArgs a, int inlin
     *a.free_count_out = top - total.take;
   }
   for (int n = tid; n < inline_rows; n += kThreads) {
-    if (n >= total.rows) {
+    if (n >= (int)total.rows) {
       write_padding(a, n);
       continue;
     }
@@ -260,29 +290,53 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanArgs a, int inlin
   }
 }
 
-// Many rows: a thread per four consecutive rows, found by one search.
+// Many rows: a thread per four consecutive rows.  The CTA counts the sequences
+// that start at or before its first row; from there a thread steps on.
 constexpr int kRowsPerThread = 4;
 
 __global__ void __launch_bounds__(256) plan_rows_kernel(PlanArgs a) {
   griddep_wait();
   griddep_launch_dependents();
-  const int n0 = (blockIdx.x * blockDim.x + threadIdx.x) * kRowsPerThread;
+  const int cta0 = blockIdx.x * blockDim.x * kRowsPerThread;
+  const int n0 = cta0 + threadIdx.x * kRowsPerThread;
   const int total = a.row_start[a.batch];
+  int b = -1;
+  for (int base = 0; base < a.batch; base += blockDim.x) {
+    const int q = base + threadIdx.x;
+    const int starts = __syncthreads_count(q < a.batch && a.row_start[q] <= cta0);
+    b += starts;
+    if (starts < (int)blockDim.x) break;
+  }
   const int end = min(a.max_rows, n0 + kRowsPerThread);
   if (n0 >= end) return;
-  int b = -1, s0 = 0, s1 = 0, len = 0, k = -1, page = -1;
+  int s0 = 0, s1 = 0, len = 0, k = -1, page = -1;
+  auto reach = [&](int n) {                     // the sequence of row n < total
+    int next = a.row_start[b + 1];
+    while (next <= n) next = a.row_start[++b + 1];
+    s0 = a.row_start[b];
+    s1 = next;
+    len = a.kv_lens[b] - (s1 - s0);
+    k = -1;
+  };
+  if (n0 < total) reach(n0);
+  // a prompt's rows: four at once where they lie in one sequence and page
+  const int row = len + n0 - s0;
+  if (end - n0 == kRowsPerThread && end <= s1 && (row & 63) <= 64 - kRowsPerThread && !a.parents && !a.mask &&
+      !a.seq_ids && ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) & 15) == 0) {
+    page = a.block_table[(size_t)b * a.max_pages + (row >> 6)];
+    const bool ok = page >= 0 && page < a.num_pages;
+    if (!ok) flag_error(a.err, MLA_DEVERR_PAGE);
+    const int sl = page * 64 + (row & 63);
+    *reinterpret_cast<int4*>(a.slots + n0) = ok ? make_int4(sl, sl + 1, sl + 2, sl + 3) : make_int4(-1, -1, -1, -1);
+    *reinterpret_cast<int4*>(a.positions + n0) = make_int4(row, row + 1, row + 2, row + 3);
+    return;
+  }
   for (int n = n0; n < end; ++n) {
     if (n >= total) {
       write_padding(a, n);
       continue;
     }
-    if (n >= s1) {                              // the first row, or past its sequence's end
-      b = find_seq(a.row_start, a.batch, n);
-      s0 = a.row_start[b];
-      s1 = a.row_start[b + 1];
-      len = a.kv_lens[b] - (s1 - s0);
-      k = -1;
-    }
+    if (n >= s1) reach(n);
     const int i = n - s0;
     if ((len + i) >> 6 != k) {
       k = (len + i) >> 6;
