@@ -74,9 +74,13 @@ constexpr int kMAbort = kMTmem + 4;
 constexpr int kMRedMax = kMTmem + 16;     // float [2 tile parities][4 parts][64 rows]
 constexpr int kMRedSum = kMRedMax + 2 * 4 * kHM * 4;    // float [4 parts][64 rows]
 constexpr int kMRedSc = kMRedSum + 4 * kHM * 4;         // float [2 tile parities][8 softmax warps]: 8-bit MMAs
-constexpr int kMScan = kMRedSc + 4 * 2 * kSoftWarps;    // int [16]: per-warp sums of the schedule's scan
-constexpr int kMPart = kMScan + 4 * 16;                 // int [4]: this pair's first sequence and its base tile
-constexpr int kMiscBytes = kMPart + 4 * 4;
+constexpr int kMaxPairs = 96;             // bound of the workspace's partials, whatever the GPU's SM count
+constexpr int kMaxDealt = 1024;           // sequences whose row tiles can be dealt out (their prefix sums are kept)
+constexpr int kMScan = kMRedSc + 4 * 2 * kSoftWarps;    // int2 [16]: per-warp sums of the schedule's scan
+constexpr int kMPart = kMScan + 8 * 16;                 // int [8]: where this pair's part begins (see there)
+constexpr int kMCol = kMPart + 4 * 8;                   // int [96]: tiles of each column
+constexpr int kMRt = kMCol + 4 * kMaxPairs;             // int [1024]: row tiles before each sequence
+constexpr int kMiscBytes = kMRt + 4 * kMaxDealt;
 
 template <bool D8>
 struct TreeLayout {
@@ -204,8 +208,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   float* red_max = reinterpret_cast<float*>(misc + kMRedMax);
   float* red_sum = reinterpret_cast<float*>(misc + kMRedSum);
   float* red_sc = reinterpret_cast<float*>(misc + kMRedSc);
-  int* scan = reinterpret_cast<int*>(misc + kMScan);
+  int2* scan = reinterpret_cast<int2*>(misc + kMScan);
   int* part0 = reinterpret_cast<int*>(misc + kMPart);
+  int* col = reinterpret_cast<int*>(misc + kMCol);
+  int* rt_before = reinterpret_cast<int*>(misc + kMRt);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t lim = p.wait_limit;
@@ -240,46 +246,107 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   griddep_wait();
   griddep_launch_dependents();
 
-  // ---- this pair's part [g0, g1) of the list of tiles: a scan over the
-  // sequences' tile counts, each thread a run of consecutive sequences
-  int total, g0, g1, used;
+  // ---- this pair's part [g0, g1) of the list of tiles, from a scan over the
+  // sequences' tile counts (each thread a run of consecutive sequences).  With
+  // more row tiles than pairs the list is dealt out: it runs down `stride`
+  // columns, column c holding the row tiles c, c + stride, ... in the order of
+  // the sequences.  Pairs next to each other then work on row tiles next to
+  // each other, those of one sequence, at about the same time, and its rows
+  // come from HBM once.
+  int total, g0, g1, used, stride, row_tiles = 0;
   {
     const int per = (p.batch + kThreads - 1) / kThreads;
     const int b_lo = min(p.batch, (int)threadIdx.x * per), b_hi = min(p.batch, b_lo + per);
-    int sum = 0;
+    int2 sum = make_int2(0, 0);             // tiles (row tiles x cached tiles), row tiles
     for (int b = b_lo; b < b_hi; ++b) {
       const SeqInfo q = seq_info(p, b);
       if (q.bad && blockIdx.x == 0) flag_error(p.err, MLA_DEVERR_POSITION);
-      sum += q.rt * q.kt;
+      sum.x += q.rt * q.kt;
+      sum.y += q.rt;
     }
-    int inc = sum;
+    int2 inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
+      const int2 v = make_int2(__shfl_up_sync(0xffffffffu, inc.x, o), __shfl_up_sync(0xffffffffu, inc.y, o));
+      if (lane >= o) inc = make_int2(inc.x + v.x, inc.y + v.y);
     }
     if (lane == 31) scan[warp] = inc;
+    if (threadIdx.x < kMaxPairs) col[threadIdx.x] = 0;
     __syncthreads();
-    int before = 0;
+    int2 base = make_int2(inc.x - sum.x, inc.y - sum.y);
     total = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += scan[w];
-      total += scan[w];
+      const int2 v = scan[w];
+      if (w < warp) base = make_int2(base.x + v.x, base.y + v.y);
+      total += v.x;
+      row_tiles += v.y;
     }
     used = min(n_pairs, total);
     g0 = pair < used ? (int)((long long)pair * total / used) : total;
     g1 = pair < used ? (int)((long long)(pair + 1) * total / used) : total;
-    int base = before + inc - sum;
-    if (g0 < g1 && base <= g0 && g0 < base + sum) {
+    const bool dealt = row_tiles > n_pairs && row_tiles <= 64 * n_pairs && p.batch <= kMaxDealt;
+    stride = dealt ? n_pairs : 1;
+    // part0: row tile index, cached tile within it, tiles to the end of its
+    // column, its sequence, row tiles before that sequence
+    if (dealt) {
+      int before = base.y;
+      for (int b = b_lo; b < b_hi; ++b) {
+        const SeqInfo q = seq_info(p, b);
+        rt_before[b] = before;
+        for (int x = 0; x < min(q.rt, stride); ++x)      // q.rt row tiles over consecutive columns
+          atomicAdd(col + (before + x) % stride, q.kt * ((q.rt - x + stride - 1) / stride));
+        before += q.rt;
+      }
+      __syncthreads();
+      if (warp == 0 && g0 < g1) {
+        int at = 0, c = 0;                               // tiles before column c
+        for (; g0 >= at + col[c]; ++c) at += col[c];
+        const int end = at + col[c];
+        for (int j0 = 0;; j0 += 32) {                    // a lane per row tile of the column
+          const int idx = c + (j0 + lane) * stride;
+          int kt = 0;
+          if (idx < row_tiles) {
+            int lo = 0, hi = p.batch - 1;
+            while (lo < hi) {
+              const int mid = (lo + hi + 1) >> 1;
+              if (rt_before[mid] <= idx) lo = mid; else hi = mid - 1;
+            }
+            kt = seq_info(p, lo).kt;
+          }
+          int upto = kt;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+          }
+          const uint32_t past = __ballot_sync(0xffffffffu, at + upto > g0);
+          if (past) {
+            if (lane == __ffs(past) - 1) {
+              part0[0] = idx;
+              part0[1] = g0 - (at + upto - kt);
+              part0[2] = end - g0;
+            }
+            break;
+          }
+          at += __shfl_sync(0xffffffffu, upto, 31);
+        }
+      }
+    } else if (g0 < g1 && base.x <= g0 && g0 < base.x + sum.x) {
       int b = b_lo;
       for (;; ++b) {
         const SeqInfo q = seq_info(p, b);
-        if (g0 < base + q.rt * q.kt) break;
-        base += q.rt * q.kt;
+        if (g0 < base.x + q.rt * q.kt) {
+          const int rt = (g0 - base.x) / q.kt;
+          part0[0] = base.y + rt;
+          part0[1] = g0 - base.x - rt * q.kt;
+          part0[2] = total - g0;
+          part0[3] = b;
+          part0[4] = base.y;
+          break;
+        }
+        base = make_int2(base.x + q.rt * q.kt, base.y + q.rt);
       }
-      part0[0] = b;
-      part0[1] = base;
     }
     if (leader && threadIdx.x == 0) p.desc[pair].follow = 0;   // a segment below may set it
   }
@@ -289,50 +356,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc + kMTmem);
 
   // ---- the pair's segments: every role walks the same sequence of them.  A
-  // first segment that continues a row tile goes last: so every pair begins at
-  // the first cached row of a row tile, and pairs that work on row tiles of
-  // one sequence read the same rows at about the same time, from L2 (two
-  // sequences of 131072 rows with 32 row tiles each: 2.69 -> 2.30 ms a call).
+  // part that begins inside a column (or inside a row tile, where it does not
+  // reach the next column) puts that beginning off to its end: so every pair
+  // starts at the first cached row of a row tile, the pairs on one sequence
+  // read the same rows at about the same time, and they come from L2 (two
+  // sequences of 131072 rows with 32 row tiles each: 2.69 -> 2.30 ms a call;
+  // 64 sequences with 5 to 16: %%%).
   struct Seg { int b, start, n, L, row, k0, nt, kt, g; };
-  struct Walk { int b, base, g, end, wrap_b, wrap_base, wrap_end; };
+  struct Stretch { int idx, k, left, g, b, rt0; };   // row tile, cached tile, tiles, list position; sequence
+  struct Walk { Stretch now, later; };
+  // the sequence of row tile w.idx
+  auto locate = [&](Stretch& w) -> SeqInfo {
+    if (stride > 1) {
+      int lo = 0, hi = p.batch - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (rt_before[mid] <= w.idx) lo = mid; else hi = mid - 1;
+      }
+      w.b = lo;
+      w.rt0 = rt_before[lo];
+      return seq_info(p, lo);
+    }
+    SeqInfo q = seq_info(p, w.b);
+    while (w.idx >= w.rt0 + q.rt) {
+      w.rt0 += q.rt;
+      q = seq_info(p, ++w.b);
+    }
+    return q;
+  };
   auto walk_begin = [&]() -> Walk {
-    Walk w{part0[0], part0[1], g0, g1, 0, 0, 0};
+    Walk w{{0, 0, 0, 0, 0, 0}, {0, 0, 0, 0, 0, 0}};
     if (g0 >= g1) return w;
-    const SeqInfo q = seq_info(p, w.b);
-    const int into = (g0 - w.base) % q.kt;
-    const int next = g0 + q.kt - into;           // where the next row tile begins
-    if (into == 0 || next >= g1) return w;       // nothing to put off, or nothing else to do
-    w.wrap_b = w.b;
-    w.wrap_base = w.base;
-    w.wrap_end = next;
-    w.g = next;
+    w.now = Stretch{part0[0], part0[1], g1 - g0, g0, part0[3], part0[4]};
+    const int to_col = part0[2], len = g1 - g0;
+    int off = 0, next = 0;
+    if (stride > 1 && to_col < len && (w.now.idx >= stride || w.now.k > 0)) {
+      off = to_col;                                // to the next column's first row tile
+      next = w.now.idx % stride + 1;
+    } else if (w.now.k > 0) {
+      const int rest = locate(w.now).kt - w.now.k; // to the column's next row tile
+      if (rest < min(len, to_col)) {
+        off = rest;
+        next = w.now.idx + stride;
+      }
+    }
+    if (off > 0) {
+      w.later = w.now;
+      w.later.left = off;
+      w.now.idx = next;
+      w.now.k = 0;
+      w.now.left = len - off;
+      w.now.g = g0 + off;
+    }
     return w;
   };
   auto next_seg = [&](Walk& w, Seg& s) -> bool {
-    if (w.g >= w.end) {
-      if (w.wrap_end == 0) return false;
-      w.b = w.wrap_b;
-      w.base = w.wrap_base;
-      w.g = g0;
-      w.end = w.wrap_end;
-      w.wrap_end = 0;
+    if (w.now.left == 0) {
+      if (w.later.left == 0) return false;
+      w.now = w.later;
+      w.later.left = 0;
     }
-    SeqInfo q = seq_info(p, w.b);
-    while (w.g >= w.base + q.rt * q.kt) {
-      w.base += q.rt * q.kt;
-      q = seq_info(p, ++w.b);
-    }
-    const int at = w.g - w.base, rt = at / q.kt;
-    s.b = w.b;
+    const SeqInfo q = locate(w.now);
+    s.b = w.now.b;
     s.start = q.start;
     s.n = q.n;
     s.L = q.L;
-    s.row = rt * kM;                       // first (node, head) row of the tile within the sequence
-    s.k0 = at - rt * q.kt;
+    s.row = (w.now.idx - w.now.rt0) * kM;  // first (node, head) row of the tile within the sequence
+    s.k0 = w.now.k;
     s.kt = q.kt;
-    s.nt = min(q.kt - s.k0, w.end - w.g);
-    s.g = w.g;
-    w.g += s.nt;
+    s.nt = min(q.kt - s.k0, w.now.left);
+    s.g = w.now.g;
+    w.now.left -= s.nt;
+    w.now.g += s.nt;
+    w.now.k = 0;
+    const int idx = w.now.idx + stride;
+    // past a column's end the next one begins (a stretch of several columns)
+    w.now.idx = stride > 1 && idx >= row_tiles ? w.now.idx % stride + 1 : idx;
     return true;
   };
 
@@ -1175,8 +1274,6 @@ __global__ void __launch_bounds__(512) tree_merge_f32_kernel(TreeParams p, int s
 }
 
 // ------------------------------------------------------------------ host side
-constexpr long long kMaxPairs = 96;     // bound of the workspace's partials, whatever the GPU's SM count
-
 // Splits of the fp32 form: enough CTAs for four per SM of a B200, at most 64.
 int splits_f32(long long rows, int n_heads) {
   const long long ctas = rows * ((n_heads + kSimtHeads - 1) / kSimtHeads);
