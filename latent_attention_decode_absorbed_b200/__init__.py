@@ -339,3 +339,4 @@ def mla_test_set_decode_wait(limit_cycles=0, withhold_q_load=False):
     _check("mla_test_set_decode_wait", lib().mla_test_set_decode_wait(int(limit_cycles), int(bool(withhold_q_load))))
 
 from .step import DecodeStep  # noqa: E402,F401
+from .tree import StepPlan, TreeDecodeStep  # noqa: E402,F401

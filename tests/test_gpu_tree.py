@@ -157,6 +157,9 @@ CASES = [
     ("heads65", "bf16", 65, [2, 3, 4], [190, 191, 192], "chain_mask"),
     ("wide_tree", "bf16", 32, [130, 65], [33, 400], "random"),
     ("many_seqs", "bf16", 24, [1 + (7 * i) % 5 for i in range(400)], [(37 * i) % 300 for i in range(400)], "tree"),
+    ("dealt_out", "bf16", 128, [1 + (5 * i) % 9 for i in range(30)], [(211 * i) % 1500 for i in range(30)], "tree"),
+    ("more_seqs_than_dealt", "bf16", 40, [1 + i % 2 for i in range(1100)], [(37 * i) % 300 for i in range(1100)],
+     "chain"),
     ("split_tiles", "bf16", 128, [20, 20], [3000, 9000], "tree"),
     ("e4m3_one", "e4m3", 128, [1], [0], "tree"),
     ("e4m3_ragged", "e4m3", 128, [5, 0, 9, 1], [70, 40, 0, 2500], "tree"),
