@@ -120,7 +120,7 @@ struct TreeParams {
   float scale_log2;             // softmax_scale * log2(e)
   const float* cache_scale;     // e4m3 cache: per-row dequantisation scale [num_pages * 64]
   const float* q_scale;         // 8-bit MMAs: scale of the two-term query per (node, head)
-  float* part_o;                // [2 pairs][128][512]
+  float* part_o;                // [2 pairs][128 x 512], in the order of part_at
   float* part_lse;              // [2 pairs][128]
   TreeDesc* desc;               // [pairs]
   void* o_lat;                  // [n_rows, n_heads, 512], bf16 or fp32
@@ -179,6 +179,12 @@ __device__ __forceinline__ int page_or_minus1(const TreeParams& p, int b, int pi
   const int pg = pidx < p.max_pages ? p.block_table[(size_t)b * p.max_pages + pidx] : -1;
   return pg >= 0 && pg < p.num_pages ? pg : -1;
 }
+
+// Partials are stored as the softmax warps read them from TMEM: 32 rows per
+// warp, a row per lane, in 4-channel pieces.  Index (in float4, of lane 0) of
+// piece `q` (0..31) of the 128 channels 256 ch + 128 (q4 >> 1) of the rows
+// 64 rank + 32 (q4 & 1) + (0..31) of a row tile.
+__device__ __forceinline__ int part_at(int rank, int ch, int q4, int q) { return (((rank * 2 + ch) * 4 + q4) * 32 + q) * 32; }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -899,10 +905,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
           }
-        } else {
-          float* base = whole ? reinterpret_cast<float*>(p.o_lat) + ((size_t)s.start * p.n_heads + s.row) * MLA_D_C
-                              : p.part_o + (size_t)slot * kM * MLA_D_C;
-          float* dst = base + (size_t)row_w * MLA_D_C + dim0 + 4 * rd_q;
+        } else if (whole) {
+          float* dst = reinterpret_cast<float*>(p.o_lat) + ((size_t)s.start * p.n_heads + s.row + row_w) * MLA_D_C +
+                       dim0 + 4 * rd_q;
 #pragma unroll 1
           for (int c4 = 0; c4 < 4; ++c4) {
             float o[32];
@@ -921,6 +926,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     *reinterpret_cast<const float4*>(tile + j * 128 + ((rd_q ^ (j & 7)) << 4));
             }
             __syncwarp();
+          }
+        } else {
+          // a partial keeps the order in which the lanes hold it (see part_at): whole lines, nothing to move
+          float4* dst = reinterpret_cast<float4*>(p.part_o + (size_t)slot * kM * MLA_D_C) +
+                        part_at((int)rank, ch, q4, 0) + lane;
+#pragma unroll 1
+          for (int c2 = 0; c2 < 2; ++c2) {
+            float o[64];
+            tmem_ld<32>(oc + 64 * c2, o);
+            tmem_ld<32>(oc + 64 * c2 + 32, o + 32);
+            tmem_wait_ld();
+            if (my < seq_rows)
+#pragma unroll
+              for (int q = 0; q < 16; ++q)
+                dst[32 * (16 * c2 + q)] =
+                    make_float4(o[4 * q] * inv_l, o[4 * q + 1] * inv_l, o[4 * q + 2] * inv_l, o[4 * q + 3] * inv_l);
           }
         }
         // this warp's part of O has been read: the pair's next segment may overwrite it
@@ -959,15 +980,18 @@ __device__ __forceinline__ void store4(__nv_bfloat16* dst, float4 v, float f) {
 
 // Joins the partials of the row tiles that crossed a pair's border: pair p's
 // last segment (slot 2 p + 1) and the first segments (slot 2 q) of the pairs
-// that follow it.  CTA (p, y): rows 2 y and 2 y + 1 of pair p's row tile, 128
-// threads x 4 channels per row.  Each partial is read once, and a call of few
-// tiles is bound by latency: a descriptor, then all parts' loads at once (the
-// weights are worked out while the values are on their way).
-constexpr int kMergeRows = 2;
-constexpr int kMergeBatch = 16;
+// that follow it.  A warp takes 32 rows of pair p's row tile, a lane each (the
+// partials' order), and 8 channels of them; CTA (p, y) has eight of the
+// tile's 256 such pieces.  Each partial is read once, and a call of few tiles
+// is bound by latency: a descriptor, then kBatch parts' loads at once.  The
+// launch takes 16 where a row tile is likely cut into more than four parts
+// (16 parts: 25.2 us a call with 8 at a time, 23.1 with 16), else 4, which
+// leaves room for more warps (two or three parts: 137 us with 16, 126 with 4).
+constexpr int kMergeWarps = 8;
+constexpr int kMergePieces = 256;
 
-template <typename OT>
-__global__ void __launch_bounds__(128 * kMergeRows) tree_merge_kernel(const float* __restrict__ part_o,
+template <typename OT, int kBatch>
+__global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const float* __restrict__ part_o,
                                                                       const float* __restrict__ part_lse,
                                                                       const TreeDesc* __restrict__ desc,
                                                                       OT* __restrict__ o_lat,
@@ -976,51 +1000,61 @@ __global__ void __launch_bounds__(128 * kMergeRows) tree_merge_kernel(const floa
   griddep_launch_dependents();
   const int pair = blockIdx.x;
   const TreeDesc d = desc[pair];
-  const int j = blockIdx.y * kMergeRows + (threadIdx.x >> 7);
-  const int c = threadIdx.x & 127, lane = threadIdx.x & 31;
-  if (d.follow == 0 || j >= d.rows) return;
+  if (d.follow == 0) return;
+  const int lane = threadIdx.x & 31, piece = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  const int rank = piece >> 7, q4 = (piece >> 5) & 3, ch = (piece >> 4) & 1, q = 2 * (piece & 15);
+  const int row = 64 * rank + 32 * (q4 & 1) + lane;      // of the row tile
+  if (row - lane >= d.rows) return;
   const int parts = d.follow + 1;
-  auto slot = [&](int k) { return k == 0 ? 2 * pair + 1 : 2 * (pair + k); };
-  // lane k of each warp holds the log-normalisers of parts k, k + 32, ... (at most 96 pairs)
-  float ls[3];
-  float mx = -INFINITY;
+  auto slot = [&](int k) -> size_t { return k == 0 ? 2 * pair + 1 : 2 * (pair + k); };
+  const float4* src = reinterpret_cast<const float4*>(part_o) + part_at(rank, ch, q4, q) + lane;
+  float mx = -INFINITY, sum = 0.f;
+  float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int k0 = 0; k0 < parts; k0 += kBatch) {
+    float4 v[kBatch][2];
+    float w[kBatch];
 #pragma unroll
-  for (int t = 0; t < 3; ++t) {
-    const int k = lane + 32 * t;
-    ls[t] = k < parts ? part_lse[slot(k) * kM + j] : -INFINITY;
-  }
-  float sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = 0; k0 < parts; k0 += kMergeBatch) {
-    float4 v[kMergeBatch];
-#pragma unroll
-    for (int k = 0; k < kMergeBatch; ++k)
-      v[k] = k0 + k < parts ? reinterpret_cast<const float4*>(part_o + ((size_t)slot(k0 + k) * kM + j) * MLA_D_C)[c]
-                            : make_float4(0.f, 0.f, 0.f, 0.f);
-    if (k0 == 0) {
-      mx = warp_max(fmaxf(fmaxf(ls[0], ls[1]), ls[2]));
-#pragma unroll
-      for (int t = 0; t < 3; ++t) {
-        ls[t] = mx == -INFINITY ? 0.f : expf(ls[t] - mx);
-        sum += ls[t];
+    for (int k = 0; k < kBatch; ++k) {
+      w[k] = -INFINITY;
+      if (k0 + k < parts) {
+        const size_t sl = slot(k0 + k);
+        w[k] = part_lse[sl * kM + row];
+        v[k][0] = src[sl * (kM * MLA_D_C / 4)];
+        v[k][1] = src[sl * (kM * MLA_D_C / 4) + 32];
+      } else {
+        v[k][0] = v[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      sum = warp_sum(sum);
     }
+    // what was joined so far is scaled to the new maximum
+    float top = mx;
 #pragma unroll
-    for (int k = 0; k < kMergeBatch; ++k) {
-      const int t = (k0 + k) >> 5;
-      const float w = __shfl_sync(0xffffffffu, t == 0 ? ls[0] : t == 1 ? ls[1] : ls[2], (k0 + k) & 31);
-      acc.x = fmaf(w, v[k].x, acc.x);
-      acc.y = fmaf(w, v[k].y, acc.y);
-      acc.z = fmaf(w, v[k].z, acc.z);
-      acc.w = fmaf(w, v[k].w, acc.w);
+    for (int k = 0; k < kBatch; ++k) top = fmaxf(top, w[k]);
+    if (top == -INFINITY) continue;          // nothing seen so far
+    const float old = expf(mx - top);
+    mx = top;
+    sum *= old;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) acc[i] = make_float4(acc[i].x * old, acc[i].y * old, acc[i].z * old, acc[i].w * old);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float wk = expf(w[k] - mx);
+      sum += wk;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        acc[i].x = fmaf(wk, v[k][i].x, acc[i].x);
+        acc[i].y = fmaf(wk, v[k][i].y, acc[i].y);
+        acc[i].z = fmaf(wk, v[k][i].z, acc[i].z);
+        acc[i].w = fmaf(wk, v[k][i].w, acc[i].w);
+      }
     }
   }
+  if (row >= d.rows) return;
   const float inv = sum > 0.f ? 1.0f / sum : 0.f;
-  const size_t row = (size_t)d.row0 + j;
-  OT* dst = o_lat + row * MLA_D_C + 4 * c;
-  store4(dst, acc, inv);
-  if (lse_out && c == 0) lse_out[row] = sum > 0.f ? mx + logf(sum) : -INFINITY;
+  const size_t out = (size_t)d.row0 + row;
+  const int dim = 256 * ch + 128 * (q4 >> 1) + 4 * q;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) store4(o_lat + out * MLA_D_C + dim + 4 * i, acc[i], inv);
+  if (lse_out && dim == 0) lse_out[out] = sum > 0.f ? mx + logf(sum) : -INFINITY;
 }
 
 // The two-term e4m3 query of the 8-bit form: per (node, head) vector
@@ -1351,12 +1385,18 @@ cudaError_t launch_tc(const TreeArgs& a, TreeParams p, const void* q8, cudaStrea
   if (pairs > most) pairs = most;
   e = launch_dependent(decode_tree_kernel<D8>, dim3((unsigned)(2 * pairs)), dim3(kThreads), smem, st, tc, tc2, tq, p);
   if (e != cudaSuccess || pairs == 1) return e;    // one pair leaves no partials
-  const dim3 grid((unsigned)pairs, kM / kMergeRows);
-  if (a.o_dtype == MLA_F32)
-    return launch_dependent(tree_merge_kernel<float>, grid, dim3(128 * kMergeRows), 0, st, p.part_o, p.part_lse,
-                            p.desc, static_cast<float*>(p.o_lat), p.lse);
-  return launch_dependent(tree_merge_kernel<__nv_bfloat16>, grid, dim3(128 * kMergeRows), 0, st, p.part_o, p.part_lse,
-                          p.desc, static_cast<__nv_bfloat16*>(p.o_lat), p.lse);
+  const dim3 grid((unsigned)pairs, kMergePieces / kMergeWarps);
+  // the parts of a row tile: the pairs over the row tiles there are room for
+  const bool many = pairs > 4 * (((long long)a.rows * a.n_heads + kM - 1) / kM);
+  auto merge = [&](auto kernel, auto* o) {
+    return launch_dependent(kernel, grid, dim3(32 * kMergeWarps), 0, st, p.part_o, p.part_lse, p.desc, o, p.lse);
+  };
+  if (a.o_dtype == MLA_F32) {
+    float* o = static_cast<float*>(p.o_lat);
+    return many ? merge(tree_merge_kernel<float, 16>, o) : merge(tree_merge_kernel<float, 4>, o);
+  }
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o_lat);
+  return many ? merge(tree_merge_kernel<__nv_bfloat16, 16>, o) : merge(tree_merge_kernel<__nv_bfloat16, 4>, o);
 }
 
 }  // namespace
