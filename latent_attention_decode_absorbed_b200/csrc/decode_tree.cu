@@ -452,6 +452,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       Walk w = walk_begin();
       Seg s;
       while (ok && next_seg(w, s)) {
+        const int32_t* bt = p.block_table + (size_t)s.b * p.max_pages;
+        const int pb = 4 * s.k0;      // the segment's first page index
+        auto entry = [&](int pidx) -> int { return pidx < p.max_pages ? bt[pidx] : -1; };
+        int cur[4], nxt[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          cur[q] = entry(pb + q);
+          nxt[q] = entry(pb + 4 + q);
+        }
         // the previous segment's score MMAs must be done with Q (both halves)
         if (uc > 0) ok = mbar_wait<false>(bar(kBQFree), (uc - 1) & 1, abort_flag, lim);
         if (!ok) break;
@@ -469,9 +478,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int c = 0; c < kChunks; ++c) tma_load_2d_pair(s_q + c * kQChunk, &tm_q, 64 * c, row, q_bar);
           }
         }
-        const int32_t* bt = p.block_table + (size_t)s.b * p.max_pages;
-        const int pb = 4 * s.k0;      // the segment's first page index
-        auto entry = [&](int pidx) -> int { return pidx < p.max_pages ? bt[pidx] : -1; };
         // rows outside the table or the pool read page 0 (readable; they are masked)
         auto page = [&](int pg) -> int { return pg >= 0 && pg < p.num_pages ? pg : 0; };
         auto take = [&](uint32_t& dst, uint32_t& fb) -> bool {
@@ -508,12 +514,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           return true;
         };
-        int cur[4], nxt[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          cur[q] = entry(pb + q);
-          nxt[q] = entry(pb + 4 + q);
-        }
         ok = load_s(page(rank ? cur[2] : cur[0]), page(rank ? cur[3] : cur[1]));
         for (int i = 0; i < s.nt && ok; ++i) {
           int ahead[4];
