@@ -58,8 +58,14 @@ __device__ __forceinline__ RawRow<IN> load_raw(const AppendArgs& a, const int32_
   return w;
 }
 
+// CTAs per SM: four where 64 registers hold a row, the next one and the gains
+// without spilling (65536 rows to bf16: 36.6 us with three, 32.0 with four;
+// 6000 rows to e4m3: 4.6 with three, 5.7 with four).
 template <typename IN, int CK>
-__global__ void __launch_bounds__(256) append_slots_kernel(AppendArgs a, const int32_t* __restrict__ slots) {
+constexpr int kSlotCtas = sizeof(IN) == 2 && CK != MLA_E4M3 ? 4 : 3;
+
+template <typename IN, int CK>
+__global__ void __launch_bounds__(256, kSlotCtas<IN, CK>) append_slots_kernel(AppendArgs a, const int32_t* __restrict__ slots) {
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -88,17 +94,20 @@ __global__ void __launch_bounds__(256) append_slots_kernel(AppendArgs a, const i
   }
 }
 
+template <typename IN, int CK>
+cudaError_t launch_slots(const AppendArgs& a, const int32_t* slots, cudaStream_t st) {
+  // one row per warp while that fits the GPU, else a grid that fills it
+  const long long rows_ctas = ((long long)a.n_new + 7) / 8, most = 2 * sm_pair_count() * kSlotCtas<IN, CK>;
+  const long long ctas = rows_ctas < most ? rows_ctas : most;
+  return launch_dependent(append_slots_kernel<IN, CK>, dim3((unsigned)ctas), dim3(256), 0, st, a, slots);
+}
+
 template <typename IN>
 cudaError_t launch_slots_in(const AppendArgs& a, const int32_t* slots, cudaStream_t st) {
-  // one row per warp while that fits the GPU, else a grid that fills it
-  long long ctas = ((long long)a.n_new + 7) / 8;
-  const long long most = 2 * sm_pair_count() * 3;
-  if (ctas > most) ctas = most;
-  const dim3 block(256), grid((unsigned)ctas);
   switch (a.cache_dtype) {
-    case MLA_F32: return launch_dependent(append_slots_kernel<IN, MLA_F32>, grid, block, 0, st, a, slots);
-    case MLA_BF16: return launch_dependent(append_slots_kernel<IN, MLA_BF16>, grid, block, 0, st, a, slots);
-    default: return launch_dependent(append_slots_kernel<IN, MLA_E4M3>, grid, block, 0, st, a, slots);
+    case MLA_F32: return launch_slots<IN, MLA_F32>(a, slots, st);
+    case MLA_BF16: return launch_slots<IN, MLA_BF16>(a, slots, st);
+    default: return launch_slots<IN, MLA_E4M3>(a, slots, st);
   }
 }
 
