@@ -391,8 +391,9 @@ size_t mla_decode_tree_workspace_bytes(mla_dtype cache_dtype, int max_rows, int 
  *               that a mask hides must hold finite values)
  *   kv_lens     device int32 [batch];  row_start device int32 [batch + 1], ascending
  *               from row_start[0] >= 0 to at most max_rows.  A sequence whose numbers
- *               are impossible (n_b < 0, L_b < n_b, L_b beyond its table row) is
- *               skipped and flagged MLA_DEVERR_POSITION
+ *               are impossible (L_b < n_b, L_b beyond its table row) is skipped and
+ *               flagged MLA_DEVERR_POSITION; offsets that do not ascend are flagged
+ *               too, and with them no sequence is computed (F32: the others are)
  *   tree_mask   device uint64 [max_rows, mask_words], bit k of word w: drafted row
  *               64 w + k is seen (bits at or past n_b are ignored, drafted rows past
  *               the words are not seen); NULL: row i sees the drafted rows 0..i

@@ -133,7 +133,7 @@ struct TreeParams {
 
 // One sequence's share of the problem; n = 0 (no work) where its numbers are
 // not possible ones.
-struct SeqInfo { int start, n, L, rt, kt; bool bad; };
+struct SeqInfo { int start, n, L, rt, kt; bool bad, order; };   // order: row_start is out of order here
 
 __device__ __forceinline__ SeqInfo seq_info(const TreeParams& p, int b) {
   SeqInfo s;
@@ -141,7 +141,8 @@ __device__ __forceinline__ SeqInfo seq_info(const TreeParams& p, int b) {
   s.L = p.kv_lens[b];
   s.start = r0;
   s.n = r1 - r0;
-  s.bad = r0 < 0 || r1 < r0 || r1 > p.n_rows || s.L < s.n || s.L > p.max_pages * 64;
+  s.order = r0 < 0 || r1 < r0 || r1 > p.n_rows;
+  s.bad = s.order || s.L < s.n || s.L > p.max_pages * 64;
   if (s.bad) s.n = 0;
   s.rt = (s.n * p.n_heads + kM - 1) / kM;
   s.kt = s.n > 0 ? (s.L + kTile - 1) / kTile : 0;
@@ -264,8 +265,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int per = (p.batch + kThreads - 1) / kThreads;
     const int b_lo = min(p.batch, (int)threadIdx.x * per), b_hi = min(p.batch, b_lo + per);
     int2 sum = make_int2(0, 0);             // tiles (row tiles x cached tiles), row tiles
+    bool order = false;
     for (int b = b_lo; b < b_hi; ++b) {
       const SeqInfo q = seq_info(p, b);
+      order |= q.order;
       if (q.bad && blockIdx.x == 0) flag_error(p.err, MLA_DEVERR_POSITION);
       sum.x += q.rt * q.kt;
       sum.y += q.rt;
@@ -278,7 +281,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (lane == 31) scan[warp] = inc;
     if (threadIdx.x < kMaxPairs) col[threadIdx.x] = 0;
-    __syncthreads();
+    // (row offsets out of order: no work at all, since only ascending ones
+    // bound the list by the call's rows)
+    const bool none = __syncthreads_or(order);
     int2 base = make_int2(inc.x - sum.x, inc.y - sum.y);
     total = 0;
 #pragma unroll
@@ -288,6 +293,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       total += v.x;
       row_tiles += v.y;
     }
+    if (none) total = row_tiles = 0;
     used = min(n_pairs, total);
     g0 = pair < used ? (int)((long long)pair * total / used) : total;
     g1 = pair < used ? (int)((long long)(pair + 1) * total / used) : total;

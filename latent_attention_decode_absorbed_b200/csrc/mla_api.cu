@@ -301,6 +301,9 @@ mla_status mla_decode_tree(const void* q_abs, mla_dtype q_dtype, const void* cac
               MLA_ERR_UNSUPPORTED, "mla_decode_tree: too many rows for one call");
   MLA_REQUIRE(cache_dtype != MLA_F32 || max_rows <= 65535, MLA_ERR_UNSUPPORTED,
               "mla_decode_tree: more than 65535 rows over an F32 cache");
+  // the copies address the pool by lines of 64 numbers
+  MLA_REQUIRE((long long)num_pages * (MLA_D_ROW / 64) * MLA_PAGE < (1ll << 31), MLA_ERR_UNSUPPORTED,
+              "mla_decode_tree: a pool of more than %d pages", (int)(((1ll << 31) - 1) / (MLA_D_ROW / 64 * MLA_PAGE)));
   if (max_rows == 0) return MLA_OK;
   MLA_REQUIRE(q_abs && cache && block_table && kv_lens && row_start && workspace && o_lat, MLA_ERR_INVALID_ARG,
               "mla_decode_tree: null pointer");

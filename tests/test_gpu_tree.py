@@ -255,6 +255,17 @@ def test_impossible_sequences_are_skipped():
     assert bool((p.o[4:8] == 7.0).all())
 
 
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("start", [[0, 8, 4, 12], [0, 4, 8, 99], [-1, 4, 8, 12], [0, 12, 0, 12]])
+def test_row_offsets_out_of_order_compute_nothing(start, cache):
+    p = Problem(cache, 16, [4, 4, 4], [100, 100, 100], "tree", seed=13)
+    p.row_start.copy_(_dev(np.array(start, np.int32)))
+    p.run()
+    torch.cuda.synchronize()
+    assert int(p.err.item()) & mla.MLA_DEVERR_POSITION
+    assert bool((p.o == 7.0).all()) and bool((p.lse == 7.0).all())
+
+
 def test_captured_call_follows_device_lengths():
     """One captured graph serves other lengths, row counts, masks and tables."""
     a = Problem("bf16", 128, [8, 8], [2000, 110], "tree", seed=11)
@@ -518,3 +529,63 @@ def test_commit_skips_rows_outside_the_pool():
     assert torch.equal(rows[2 * 64 + 60], old[2 * 64 + 61])
     rows[2 * 64 + 60] = old[2 * 64 + 60]
     assert torch.equal(rows, old)
+
+
+# ------------------------------------------------------------------ far pages, two calls at once
+def test_pages_past_32_bit_offsets():
+    """A pool of more than 2^32 bytes and 2^31 numbers: attention, append and commit at its far end."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(14)
+    num_pages, far = 60000, 59000
+    pool = torch.empty((num_pages, 9, 64, 64), dtype=torch.bfloat16, device="cuda")
+    pool[0].zero_()
+    p = Problem("bf16", 16, [5, 3], [200, 70], "tree", seed=14)
+    pool[far:far + p.num_pages].copy_(p.pool)
+    table = torch.where(p.table >= 0, p.table + far, p.table)
+    p.run(cache=pool, num_pages=num_pages, block_table=table)
+    p.check()
+    assert int(p.err.item()) == 0
+    # append by slot: the same bits as near the pool's start
+    n, max_pos = 100, 256
+    x = torch.randn((n, 576), generator=gen, device="cuda").to(torch.bfloat16)
+    cos = np.empty((max_pos, 32), np.float32)
+    sin = np.empty_like(cos)
+    mla.mla_rope_table(10000.0, max_pos, cos, sin)
+    cos, sin = _dev(cos), _dev(sin)
+    slots = torch.randperm(128, generator=gen, device="cuda")[:n].int()
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    near = torch.zeros((2, 9, 64, 64), dtype=torch.bfloat16, device="cuda")
+    pool[far:far + 2].zero_()
+    for dst, off in ((near, 0), (pool, far * 64)):
+        mla.mla_cache_append_slots(x, mla.MLA_BF16, n, slots + off, pos, None, 1e-6, cos, sin, max_pos, dst, None,
+                                   mla.MLA_BF16, dst.shape[0])
+    assert torch.equal(pool[far:far + 2], near)
+    # commit: the same rows
+    lens, start = _dev(np.array([110], np.int32)), _dev(np.array([0, 20], np.int32))
+    counts, nodes = _dev(np.array([3], np.int32)), _dev(np.array([1, 7, 19] + [0] * 17, np.int32))
+    for dst, t in ((near, [[1, 0]]), (pool, [[far + 1, far]])):
+        mla.mla_cache_commit(lens, start, 1, 20, counts, nodes, _dev(np.array(t, np.int32)), 2, 64, dst, None,
+                             mla.MLA_BF16, dst.shape[0])
+    torch.cuda.synchronize()
+    assert torch.equal(pool[far:far + 2], near)
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Calls with workspaces of their own on two streams give each its own result."""
+    a = Problem("bf16", 128, [9, 4], [1500, 900], "tree", seed=15)
+    b = Problem("e4m3", 64, [12, 3, 8], [700, 64, 2000], "random", seed=16)
+    want = []
+    for p in (a, b):
+        p.run()
+        torch.cuda.synchronize()
+        want.append((p.o.clone(), p.lse.clone()))
+        p.o.fill_(7.0)
+        p.lse.fill_(7.0)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        a.run(stream=s1)
+        b.run(stream=s2)
+    torch.cuda.synchronize()
+    for p, (o, lse) in zip((a, b), want):
+        assert torch.equal(p.o, o) and torch.equal(p.lse, lse)

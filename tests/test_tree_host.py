@@ -69,6 +69,7 @@ TREE = dict(q_abs=FAKE, q_dtype=mla.MLA_BF16, cache=FAKE, cache_scale=None, cach
     (dict(softmax_scale=math.inf), INV), (dict(q_dtype=mla.MLA_F32), UNS), (dict(cache_dtype=mla.MLA_F32), UNS),
     (dict(o_dtype=mla.MLA_E4M3), UNS), (dict(max_pages_per_seq=1 << 25), INV), (dict(max_rows=1 << 22), UNS),
     (dict(q_dtype=mla.MLA_F32, cache_dtype=mla.MLA_F32, max_rows=65536, n_heads=1), UNS), (dict(q_abs=None), INV),
+    (dict(num_pages=3728271), UNS),
     (dict(workspace=None), INV), (dict(o_lat=None), INV), (dict(cache_dtype=mla.MLA_E4M3), INV),
     (dict(cache=FAKE + 64), INV), (dict(workspace=FAKE + 8), INV), (dict(tree_mask=FAKE + 4), INV),
     (dict(q_abs=FAKE + 2), INV),
