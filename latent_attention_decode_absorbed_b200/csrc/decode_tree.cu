@@ -57,7 +57,8 @@ constexpr int kBox8 = 4096;               // [64 rows x 64 codes]
 constexpr int kQ8Plane = kChunks * kBox8; // one term (hi or lo) of Q, 9 x [64 rows x 64 codes]
 constexpr int kQChunk = kHM * 128;        // [64 rows x 64 dims], 16-bit
 constexpr int kPChunk = kHM * 128;        // [64 rows x 64 cached rows], 16-bit: P of one page
-constexpr int kWarpProd = 0, kWarpMma = 1, kWarpSoft0 = 2, kSoftWarps = 8;
+constexpr int kProducers = 2;             // warps 0, 1: TMA producers
+constexpr int kWarpMma = kProducers, kWarpSoft0 = kWarpMma + 1, kSoftWarps = 8;
 constexpr int kThreads = 32 * (kWarpSoft0 + kSoftWarps);
 constexpr float kRescaleLog2 = 8.0f;      // lazy rescale threshold (log2 units)
 constexpr float kRescaleLog2Q8 = 4.0f;    // 8-bit MMAs: probabilities stay <= 2^4, and times
@@ -248,7 +249,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_cache);
     tma_prefetch_desc(&tm_cache2);
   }
-  if (warp == kWarpProd) tmem_alloc_pair(s_misc + kMTmem, kTmemCols);
+  if (warp == 0) tmem_alloc_pair(s_misc + kMTmem, kTmemCols);
   // global memory only after the previous kernel on the stream has completed
   griddep_wait();
   griddep_launch_dependents();
@@ -448,9 +449,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   };
 
   uint32_t kc = 0;   // ring stages handed out (producer) or consumed (MMA)
-  if (warp == kWarpProd) {
-    // ============ TMA producer (both CTAs), in the order the MMA consumes ============
-    // S(0), then per tile i: S(i+1), O(i); boxes as in decode_pair.cu
+  if (warp < kProducers) {
+    // ============ TMA producers (both CTAs), in the order the MMA consumes ============
+    // S(0), then per tile i: S(i+1), O(i); boxes as in decode_pair.cu.  The
+    // stages go to the producers in turn: a stage's wait, expectation and
+    // copies take one lane ~430 cycles whatever their size, against 256 that
+    // its MMAs take (L2-resident rows: 922 us with one producer, 849 with two;
+    // two 131072-row sequences 1840 -> 1700).
     if (lane == 0) {
       const uint64_t pol_keep = policy_evict_last();
       uint32_t uc = 0;
@@ -468,11 +473,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           nxt[q] = entry(pb + 4 + q);
         }
         // the previous segment's score MMAs must be done with Q (both halves)
-        if (uc > 0) ok = mbar_wait<false>(bar(kBQFree), (uc - 1) & 1, abort_flag, lim);
+        if (uc > 0 && warp == 0) ok = mbar_wait<false>(bar(kBQFree), (uc - 1) & 1, abort_flag, lim);
         if (!ok) break;
         // (test hook: the leader leaves the query load of its first segment
         // out, so the MMA issuer's wait for it runs out and the launch aborts)
-        if (!(p.withhold_q && leader && uc == 0)) {
+        if (warp == 0 && !(p.withhold_q && leader && uc == 0)) {
           const int row = s.start * p.n_heads + s.row + (int)rank * kHM;
           const uint32_t q_bar = mapa(bar(kBQFull), 0);
           if (leader) mbar_arrive_expect_tx(bar(kBQFull), 2u * kChunks * kQChunk);
@@ -486,50 +491,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         // rows outside the table or the pool read page 0 (readable; they are masked)
         auto page = [&](int pg) -> int { return pg >= 0 && pg < p.num_pages ? pg : 0; };
+        // the next stage: false where it is the other producer's (or the launch aborts)
         auto take = [&](uint32_t& dst, uint32_t& fb) -> bool {
-          const uint32_t slot = kc % kSlots;
-          const uint32_t ph = (kc / kSlots) & 1u;
-          if (!mbar_wait<false>(bar(kBEmpty + slot), ph ^ 1u, abort_flag, lim)) return false;
+          const uint32_t my = kc++;
+          if ((int)(my % kProducers) != warp || !ok) return false;
+          const uint32_t slot = my % kSlots;
+          const uint32_t ph = (my / kSlots) & 1u;
+          ok = mbar_wait<false>(bar(kBEmpty + slot), ph ^ 1u, abort_flag, lim);
+          if (!ok) return false;
           if (leader) mbar_arrive_expect_tx(bar(kBFull + slot), 2u * L::kSlotB);
           dst = s_ring + slot * L::kSlotB;
           fb = mapa(bar(kBFull + slot), 0);
-          ++kc;
           return true;
         };
         // score stages: column chunk c of this CTA's two pages of the tile
-        auto load_s = [&](int pg0, int pg1) -> bool {
+        auto load_s = [&](int pg0, int pg1) {
           for (int c = 0; c < kChunks; ++c) {
             uint32_t dst, fb;
-            if (!take(dst, fb)) return false;
+            if (!take(dst, fb)) continue;
             tma_load_2d_pair_hint(dst, &tm_cache, 0, (pg0 * kChunks + c) * 64, fb, pol_keep);
             tma_load_2d_pair_hint(dst + L::kSlotB / 2, &tm_cache, 0, (pg1 * kChunks + c) * 64, fb, pol_keep);
           }
-          return true;
         };
         // value stages: per page of tile j with rows, this CTA's two pairs of dims blocks
-        auto load_o = [&](int j, const int (&pg)[4]) -> bool {
+        auto load_o = [&](int j, const int (&pg)[4]) {
 #pragma unroll
           for (int pg_i = 0; pg_i < 4; ++pg_i) {
             if (kTile * (s.k0 + j) + 64 * pg_i >= s.L) break;
             for (int bb = 0; bb < 2; ++bb) {
               uint32_t dst, fb;
-              if (!take(dst, fb)) return false;
+              if (!take(dst, fb)) continue;
               tma_load_2d_pair_hint(dst, &tm_cache2, 0, (pg[pg_i] * kChunks + 4 * bb + 2 * (int)rank) * 64, fb,
                                     pol_keep);
             }
           }
-          return true;
         };
-        ok = load_s(page(rank ? cur[2] : cur[0]), page(rank ? cur[3] : cur[1]));
+        load_s(page(rank ? cur[2] : cur[0]), page(rank ? cur[3] : cur[1]));
         for (int i = 0; i < s.nt && ok; ++i) {
           int ahead[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) ahead[q] = entry(pb + 4 * (i + 2) + q);
-          if (i + 1 < s.nt) ok = load_s(page(rank ? nxt[2] : nxt[0]), page(rank ? nxt[3] : nxt[1]));
+          if (i + 1 < s.nt) load_s(page(rank ? nxt[2] : nxt[0]), page(rank ? nxt[3] : nxt[1]));
           int pg[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) pg[q] = page(cur[q]);
-          if (ok) ok = load_o(i, pg);
+          load_o(i, pg);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             cur[q] = nxt[q];
@@ -971,7 +977,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync();
-  if (warp == kWarpProd) {
+  if (warp == 0) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);
   }
