@@ -10,7 +10,8 @@
 // into registers before any of it is written.  Since i_j >= j and the path
 // ascends, a batch's targets lie below every later batch's sources, so
 // batches in order never overwrite a row that is still to be read.  Bound by
-// latency (a few rows per sequence): path, table entries, rows, one after another.
+// latency (a few rows per sequence): path, table entries, rows, one after
+// another; 2.7 us for 64 sequences, 4.8 for 512 (from a captured graph).
 #include "mla_device.cuh"
 #include "mla_internal.h"
 

@@ -30,6 +30,18 @@
 // the workspace, which tree_merge_kernel joins.  The partials are thus
 // bounded by the number of pairs, not by the lengths or the batch.
 //
+// What bounds it.  Calls of many row tiles: the shared-memory data path, close
+// behind the tensor cores.  Per tile of 256 cached rows a CTA's MMAs take 4357
+// cycles and read 3264 x 128 bytes of operands, the copies write 2176 and the
+// softmax 256 more: 5700 cycles where one at a time passes.  Measured: 5960 to
+// 6010 cycles a tile (a full profile: tensor 45 % of elapsed cycles at 6670 a
+// tile, operand reads 44 %, LSU 7 %), 1377 TFLOP/s from L2 in a single call;
+// back to back the 1000 W cap takes the clock to ~1.6 GHz.  Calls of few row
+// tiles per sequence: HBM (64 x 8 drafts x 16 heads: 117 us of 55).  Calls of a
+// few tiles: latency (one token over 4096 rows, 20.5 us: schedule 1.7, query
+// and first rows 1.6, scores 2.5, softmax 1.0, values 1.7, epilogue 2.6, exit
+// and merge 5.5).
+//
 // With an e4m3 cache both GEMMs run on kind::f8f6f4 straight from the cache
 // codes: the query as two e4m3 terms on a power-of-two scale (split_q_tree
 // below: exact for all but tiny components, so the scores are fp32-exact
@@ -374,7 +386,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // starts at the first cached row of a row tile, the pairs on one sequence
   // read the same rows at about the same time, and they come from L2 (two
   // sequences of 131072 rows with 32 row tiles each: 2.69 -> 2.30 ms a call;
-  // 64 sequences with 5 to 16: %%%).
+  // 64 sequences of 1024 to 8192 rows with 5 to 16: 970 -> 890 us with the list
+  // dealt out, 0.73 GB read from HBM of the 0.52 that a call cannot do without).
   struct Seg { int b, start, n, L, row, k0, nt, kt, g; };
   struct Stretch { int idx, k, left, g, b, rt0; };   // row tile, cached tile, tiles, list position; sequence
   struct Walk { Stretch now, later; };
@@ -551,11 +564,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       constexpr uint32_t idS = D8 ? idesc_e4m3(kM, 256, false, false) : idesc_f16(kM, 256, false, false);
       constexpr uint32_t idO = D8 ? idesc_e4m3(kM, 256, false, true) : idesc_f16(kM, 256, false, true);
       // Stages are taken in groups (three score chunks, a page's two value
-      // boxes): the barriers of a group are looked at together.  The tensor
-      // cores hold little more than one MMA in advance, so whatever stands
-      // between a stage's last MMA and the next one's first is a gap, and a
-      // wait costs ~85 cycles even when the data is there (it is, at the first
-      // look, 99 % of the time).
+      // boxes), whose barriers are waited for together.  The tensor cores hold
+      // little more than one MMA in advance, so whatever stands between a
+      // stage's last MMA and the next one's first is a gap (two 131072-row
+      // sequences 2.30 -> 2.11 ms a call, e4m3 515 -> 492 us).
       uint32_t slot = 0, ph = 0;
       auto step = [&](uint32_t& sl, uint32_t& q) {
         if (++sl == kSlots) {

