@@ -1124,16 +1124,21 @@ __global__ void __launch_bounds__(256) split_q_tree_kernel(const __nv_bfloat16* 
 
 // ------------------------------------------------------------------ fp32 cache
 // Exact fp32 on the CUDA cores, for small models: CTA = (split of the
-// sequence's rows, group of 16 heads, node), two heads per warp so that a row
-// read from shared memory serves both; rows staged 32 at a time.  Each sequence
-// is cut into `splits` equal runs of whole 8-row groups: a call of few nodes
-// still fills the GPU, down to one group per CTA, since what bounds it is the
-// latency of a CTA's chain of loads, products and reductions.
-// tree_merge_f32_kernel joins the splits.
-constexpr int kSimtRows = 32;
+// sequence's rows, group of 16 heads, node), four heads per warp, rows staged
+// 16 at a time in shared memory while the previous 16 are worked.  Each
+// sequence is cut into `splits` equal runs of whole 8-row groups: a call of few
+// nodes still fills the GPU, down to one group per CTA, since what bounds it is
+// the latency of a CTA's chain of loads, products and reductions (4 nodes x 16
+// heads x 260 rows: 10.1 us with the merge).  Many nodes are bound by issue and
+// by the reads of the staged rows: a row that a warp reads serves four heads,
+// and four rows are worked at a time (8 sequences x 16 nodes x 32 heads x 2064
+// rows: 803 us, 22.7 TFLOP/s; two heads per warp, a row at a time and nothing
+// staged ahead: 1217 us).  tree_merge_f32_kernel joins the splits.
+constexpr int kSimtRows = 16;
 constexpr int kSimtGroup = 8;
 constexpr int kSimtHeads = 16;
-constexpr int kSimtWarps = kSimtHeads / 2;
+constexpr int kSimtPer = 4;                  // heads per warp
+constexpr int kSimtWarps = kSimtHeads / kSimtPer;
 
 // The sequence of node n (-1: n lies outside [row_start[0], row_start[batch]),
 // or the sequence's numbers are bad).
@@ -1148,43 +1153,53 @@ __device__ __forceinline__ int seq_of(const TreeParams& p, int n, SeqInfo& s) {
   return s.bad || n < s.start || n >= s.start + s.n ? -1 : lo;
 }
 
-// Sums of eight values over the warp: the value of index lane >> 2, on every lane.
-__device__ __forceinline__ float warp_sum8(const float (&v)[8]) {
+// Sums of sixteen values over the warp: the value of index lane >> 1, on every lane.
+__device__ __forceinline__ float warp_sum16(const float (&v)[16]) {
   const int lane = threadIdx.x & 31;
-  float a[4], b[2];
+  float a[8], b[4], c[2];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const bool up = lane & 16;
+    a[i] = (up ? v[i + 8] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 8], 16);
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const bool up = lane & 16;
-    a[i] = (up ? v[i + 4] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 4], 16);
+    const bool up = lane & 8;
+    b[i] = (up ? a[i + 4] : a[i]) + __shfl_xor_sync(0xffffffffu, up ? a[i] : a[i + 4], 8);
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const bool up = lane & 8;
-    b[i] = (up ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, up ? a[i] : a[i + 2], 8);
+    const bool up = lane & 4;
+    c[i] = (up ? b[i + 2] : b[i]) + __shfl_xor_sync(0xffffffffu, up ? b[i] : b[i + 2], 4);
   }
-  const bool up = lane & 4;
-  float c = (up ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, up ? b[0] : b[1], 4);
-  c += __shfl_xor_sync(0xffffffffu, c, 2);
-  c += __shfl_xor_sync(0xffffffffu, c, 1);
-  return c;
+  const bool up = lane & 2;
+  const float d = (up ? c[1] : c[0]) + __shfl_xor_sync(0xffffffffu, up ? c[0] : c[1], 2);
+  return d + __shfl_xor_sync(0xffffffffu, d, 1);
 }
 
-__global__ void __launch_bounds__(32 * kSimtWarps) decode_tree_simt_kernel(const float* __restrict__ q_abs,
-                                                                           const float* __restrict__ cache,
-                                                                           TreeParams p, int splits) {
-  extern __shared__ float tile[];            // [kSimtRows][576]
-  __shared__ long long slot_of[kSimtRows];
-  __shared__ float score[kSimtWarps][2][kSimtRows];
+// 16 bytes of global memory to shared memory, asynchronously; zeros where !from.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, bool from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
+               "r"(from ? 16 : 0)
+               : "memory");
+}
+
+__global__ void __launch_bounds__(32 * kSimtWarps, 2) decode_tree_simt_kernel(const float* __restrict__ q_abs,
+                                                                              const float* __restrict__ cache,
+                                                                              TreeParams p, int splits) {
+  extern __shared__ __align__(16) float tiles[];       // [2][kSimtRows][576]
+  __shared__ int seen_of[2][kSimtRows];
+  __shared__ __align__(16) float score[kSimtWarps][kSimtPer][kSimtRows];   // scores, then weights, of the staged rows
   griddep_wait();
   griddep_launch_dependents();
   const int split = blockIdx.x, n = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h0 = blockIdx.y * kSimtHeads + 2 * warp;
-  const int heads = min(max(p.n_heads - h0, 0), 2);      // of this warp
+  const int h0 = blockIdx.y * kSimtHeads + kSimtPer * warp;
+  const int heads = min(max(p.n_heads - h0, 0), kSimtPer);      // of this warp
   const size_t vec = (size_t)n * p.n_heads + h0;
-  float q[2][18];
+  float q[kSimtPer][18];
 #pragma unroll
-  for (int e = 0; e < 2; ++e)
+  for (int e = 0; e < kSimtPer; ++e)
 #pragma unroll
     for (int k = 0; k < 18; ++k) q[e][k] = e < heads ? q_abs[(vec + e) * MLA_D_ROW + lane + 32 * k] : 0.f;
   SeqInfo s;
@@ -1198,83 +1213,104 @@ __global__ void __launch_bounds__(32 * kSimtWarps) decode_tree_simt_kernel(const
   const int lo = (int)((long long)groups * split / splits) * kSimtGroup;
   const int hi = min((int)((long long)groups * (split + 1) / splits) * kSimtGroup, s.L);
   const uint64_t* mask = p.tree_mask ? p.tree_mask + (size_t)n * p.mask_words : nullptr;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  float o[2][16];
+  float m[kSimtPer], l[kSimtPer];
+  float o[kSimtPer][16];
 #pragma unroll
-  for (int e = 0; e < 2; ++e)
+  for (int e = 0; e < kSimtPer; ++e) {
+    m[e] = -INFINITY;
+    l[e] = 0.f;
 #pragma unroll
     for (int k = 0; k < 16; ++k) o[e][k] = 0.f;
-  for (int j0 = lo; j0 < hi; j0 += kSimtRows) {
-    const int cnt = min(kSimtRows, hi - j0);
-    __syncthreads();
-    if (threadIdx.x < kSimtRows) {
-      long long sl = -1;
-      if ((int)threadIdx.x < cnt) {
-        const int j = j0 + threadIdx.x;
-        const int pg = page_or_minus1(p, b, j >> 6);
-        if (pg >= 0) sl = (long long)pg * 64 + (j & 63);
-        else flag_error(p.err, MLA_DEVERR_PAGE);
+  }
+  // stage rows j0 .. j0 + 15: warp w rows w, w + 4, ...; rows that the node
+  // does not see (or past the end) as zeros, whatever the cache holds there
+  auto stage = [&](int j0, int buf) {
+#pragma unroll
+    for (int x = 0; x < kSimtRows / kSimtWarps; ++x) {
+      const int r = warp + kSimtWarps * x, j = j0 + r;
+      int pg = -1;
+      bool seen = false;
+      if (j < hi) {
+        pg = page_or_minus1(p, b, j >> 6);
+        if (pg < 0) flag_error(p.err, MLA_DEVERR_PAGE);
+        seen = pg >= 0 && (visible_rows(j, prefix, s.n, node, mask, p.mask_words) & 1);
       }
-      slot_of[threadIdx.x] = sl;
+      if (lane == 0) seen_of[buf][r] = seen;
+      // a row's piece c (16 bytes): block c / 16 of its page
+      const float* src = cache + ((size_t)(seen ? pg : 0) * 9 * 64 + (j & 63)) * 64;
+      const uint32_t dst = smem_u32(tiles + (buf * kSimtRows + r) * MLA_D_ROW);
+#pragma unroll
+      for (int i = 0; i < 5; ++i) {
+        const int c = lane + 32 * i;
+        if (c < MLA_D_ROW / 4) copy_async16(dst + 16 * c, src + (c >> 4) * 64 * 64 + 4 * (c & 15), seen);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (lo < hi) stage(lo, 0);
+  for (int j0 = lo, buf = 0; j0 < hi; j0 += kSimtRows, buf ^= 1) {
+    const int cnt4 = (min(kSimtRows, hi - j0) + 3) & ~3;         // rows are worked four at a time
+    if (j0 + kSimtRows < hi) {
+      stage(j0 + kSimtRows, buf ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
     __syncthreads();
-    const int cnt4 = (cnt + 3) & ~3;         // rows are worked four at a time: the rest as zeros
-    for (int i = threadIdx.x; i < cnt4 * (MLA_D_ROW / 4); i += blockDim.x) {
-      const int jj = i / (MLA_D_ROW / 4), d = 4 * (i % (MLA_D_ROW / 4));
-      const long long sl = slot_of[jj];
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (sl >= 0) x = *reinterpret_cast<const float4*>(cache + cache_index((size_t)sl, d));
-      *reinterpret_cast<float4*>(tile + jj * MLA_D_ROW + d) = x;
-    }
-    __syncthreads();
-    if (heads == 0) continue;
-    for (int jj = 0; jj < cnt4; jj += 4) {
-      float part[8];                         // [head][row]
+    const float* tile = tiles + buf * kSimtRows * MLA_D_ROW;
+    if (heads > 0) {
+      for (int jj = 0; jj < cnt4; jj += 4) {
+        float part[16];                        // [head][row]
 #pragma unroll
-      for (int x = 0; x < 8; ++x) part[x] = 0.f;
+        for (int x = 0; x < 16; ++x) part[x] = 0.f;
+        const float* rows = tile + jj * MLA_D_ROW + lane;
 #pragma unroll
-      for (int k = 0; k < 18; ++k) {
+        for (int k = 0; k < 18; ++k) {
+          float t[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float t = tile[(jj + x) * MLA_D_ROW + lane + 32 * k];
-          part[x] = fmaf(q[0][k], t, part[x]);
-          part[4 + x] = fmaf(q[1][k], t, part[4 + x]);
+          for (int x = 0; x < 4; ++x) t[x] = rows[x * MLA_D_ROW + 32 * k];
+#pragma unroll
+          for (int e = 0; e < kSimtPer; ++e)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) part[4 * e + x] = fmaf(q[e][k], t[x], part[4 * e + x]);
+        }
+        const float v = warp_sum16(part);
+        if ((lane & 1) == 0) score[warp][lane >> 3][jj + ((lane >> 1) & 3)] = v;
+      }
+      __syncwarp();
+      const bool seen = lane < kSimtRows && seen_of[buf][lane & (kSimtRows - 1)];   // row j0 + lane
+#pragma unroll
+      for (int e = 0; e < kSimtPer; ++e) {
+        const float sc = seen ? score[warp][e][lane & (kSimtRows - 1)] * p.scale_log2 : -INFINITY;   // natural units here, see the launch
+        const float mn = fmaxf(m[e], warp_max(sc));
+        const float ms = mn == -INFINITY ? 0.f : mn;      // nothing seen so far: every weight is 0
+        const float alpha = expf(m[e] - ms), pr = expf(sc - ms);
+        if (lane < kSimtRows) score[warp][e][lane] = pr;
+        l[e] = l[e] * alpha + warp_sum(pr);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[e][k] *= alpha;
+        m[e] = mn;
+      }
+      __syncwarp();
+      for (int jj = 0; jj < cnt4; jj += 4) {
+        float4 w[kSimtPer];
+#pragma unroll
+        for (int e = 0; e < kSimtPer; ++e) w[e] = *reinterpret_cast<const float4*>(&score[warp][e][jj]);
+        const float* rows = tile + jj * MLA_D_ROW + lane;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float t0 = rows[32 * k], t1 = rows[MLA_D_ROW + 32 * k], t2 = rows[2 * MLA_D_ROW + 32 * k],
+                      t3 = rows[3 * MLA_D_ROW + 32 * k];
+#pragma unroll
+          for (int e = 0; e < kSimtPer; ++e)
+            o[e][k] = fmaf(w[e].w, t3, fmaf(w[e].z, t2, fmaf(w[e].y, t1, fmaf(w[e].x, t0, o[e][k]))));
         }
       }
-      const float v = warp_sum8(part);
-      if ((lane & 3) == 0) score[warp][lane >> 4][jj + ((lane >> 2) & 3)] = v;
     }
-    __syncwarp();
-    const uint64_t vis = visible_rows(j0, prefix, s.n, node, mask, p.mask_words);
-    const bool seen = lane < cnt && slot_of[lane] >= 0 && ((vis >> lane) & 1);   // row j0 + lane
-    float pr[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float sc = seen ? score[warp][e][lane] * p.scale_log2 : -INFINITY;   // natural units here, see the launch
-      const float mn = fmaxf(m[e], warp_max(sc));
-      const float ms = mn == -INFINITY ? 0.f : mn;      // nothing seen so far: every weight is 0
-      const float alpha = expf(m[e] - ms);
-      pr[e] = expf(sc - ms);
-      l[e] = l[e] * alpha + warp_sum(pr[e]);
-#pragma unroll
-      for (int k = 0; k < 16; ++k) o[e][k] *= alpha;
-      m[e] = mn;
-    }
-    __syncwarp();
-    const uint32_t any = __ballot_sync(0xffffffffu, seen);
-    for (int jj = 0; jj < cnt; ++jj) {
-      if (!(any >> jj & 1)) continue;       // hidden rows are not touched (0 times infinity would be NaN)
-      const float p0 = __shfl_sync(0xffffffffu, pr[0], jj), p1 = __shfl_sync(0xffffffffu, pr[1], jj);
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float t = tile[jj * MLA_D_ROW + lane + 32 * k];
-        o[0][k] = fmaf(p0, t, o[0][k]);
-        o[1][k] = fmaf(p1, t, o[1][k]);
-      }
-    }
+    __syncthreads();                         // the buffer may be staged again
   }
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
+  for (int e = 0; e < kSimtPer; ++e) {
     if (e >= heads) break;
     const size_t base = (vec + e) * splits + split;
     const float inv = l[e] > 0.f ? 1.0f / l[e] : 0.f;
@@ -1455,7 +1491,7 @@ cudaError_t launch_decode_tree(const TreeArgs& a, cudaStream_t st) {
     const long long groups = (long long)a.max_pages * (64 / kSimtGroup);
     int splits = splits_f32(a.rows, a.n_heads);
     if (splits > groups) splits = (int)groups;
-    const int smem = kSimtRows * MLA_D_ROW * (int)sizeof(float);
+    const int smem = 2 * kSimtRows * MLA_D_ROW * (int)sizeof(float);
     cudaError_t e = cudaFuncSetAttribute(decode_tree_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)splits, (unsigned)((a.n_heads + kSimtHeads - 1) / kSimtHeads), (unsigned)a.rows);
