@@ -86,7 +86,9 @@ def native():
     global _marshal
     if _marshal is None:
         lib()
+        import torch
         from . import _native
+        _native.set_stream_getters(torch.cuda.current_device, torch._C._cuda_getCurrentRawStream)
         _marshal = _native
     return _marshal
 
@@ -203,10 +205,10 @@ def mla_step_plan(seq_lens, new_counts, parents, batch, max_rows, mask_words, he
     """Pages, block table, row offsets, slots, positions and ancestor masks of a
     step, from device lengths, row counts and drafted trees (parents, seq_ids
     and tree_mask may be None); tree_mask: int64 [max_rows, mask_words]."""
-    status = native().step_plan(seq_lens, new_counts, parents, batch, max_rows, mask_words, held_in, held_out,
-                                free_pages, free_count_in, free_count_out, block_table, max_pages_per_seq, page_size,
-                                num_pages, row_start, kv_lens, seq_ids, positions, slots, tree_mask, err_word,
-                                _stream(stream))
+    status = (_marshal or native()).step_plan(seq_lens, new_counts, parents, batch, max_rows, mask_words, held_in,
+                                              held_out, free_pages, free_count_in, free_count_out, block_table,
+                                              max_pages_per_seq, page_size, num_pages, row_start, kv_lens, seq_ids,
+                                              positions, slots, tree_mask, err_word, stream)
     if status:
         _check("mla_step_plan", status)
 
@@ -214,9 +216,9 @@ def mla_step_plan(seq_lens, new_counts, parents, batch, max_rows, mask_words, he
 def mla_cache_append_slots(kv_a, kv_dtype, n_new, slots, positions, norm_gain, eps, rope_cos, rope_sin,
                            rope_max_pos, cache, cache_scale, cache_dtype, num_pages, err_word=None, stream=None):
     """mla_cache_append's rows at given slots (-1: skipped), rotated to given positions."""
-    status = native().cache_append_slots(kv_a, kv_dtype, n_new, slots, positions, norm_gain, eps, rope_cos, rope_sin,
-                                         rope_max_pos, cache, cache_scale, cache_dtype, num_pages, err_word,
-                                         _stream(stream))
+    status = (_marshal or native()).cache_append_slots(kv_a, kv_dtype, n_new, slots, positions, norm_gain, eps,
+                                                       rope_cos, rope_sin, rope_max_pos, cache, cache_scale,
+                                                       cache_dtype, num_pages, err_word, stream)
     if status:
         _check("mla_cache_append_slots", status)
 
@@ -231,10 +233,10 @@ def mla_decode_tree(q_abs, q_dtype, cache, cache_scale, cache_dtype, num_pages, 
                     workspace, o_lat, o_dtype, lse_out=None, err_word=None, stream=None):
     """Attention and merge of a ragged number of drafted tokens per sequence, each
     seeing its prefix and the drafted rows of its mask (None: a chain)."""
-    status = native().decode_tree(q_abs, q_dtype, cache, cache_scale, cache_dtype, num_pages, block_table,
-                                  max_pages_per_seq, page_size, kv_lens, row_start, batch, max_rows, n_heads,
-                                  tree_mask, mask_words, softmax_scale, workspace, o_lat, o_dtype, lse_out, err_word,
-                                  _stream(stream))
+    status = (_marshal or native()).decode_tree(q_abs, q_dtype, cache, cache_scale, cache_dtype, num_pages,
+                                                block_table, max_pages_per_seq, page_size, kv_lens, row_start, batch,
+                                                max_rows, n_heads, tree_mask, mask_words, softmax_scale, workspace,
+                                                o_lat, o_dtype, lse_out, err_word, stream)
     if status:
         _check("mla_decode_tree", status)
 
@@ -244,9 +246,9 @@ def mla_cache_commit(kv_lens, row_start, batch, max_rows, accept_counts, accept_
                      err_word=None, stream=None):
     """Move each sequence's accepted path of drafted rows to the front of its
     drafted rows; seq_lens_out: the lengths after it."""
-    status = native().cache_commit(kv_lens, row_start, batch, max_rows, accept_counts, accept_nodes, block_table,
-                                   max_pages_per_seq, page_size, cache, cache_scale, cache_dtype, num_pages,
-                                   seq_lens_out, err_word, _stream(stream))
+    status = (_marshal or native()).cache_commit(kv_lens, row_start, batch, max_rows, accept_counts, accept_nodes,
+                                                 block_table, max_pages_per_seq, page_size, cache, cache_scale,
+                                                 cache_dtype, num_pages, seq_lens_out, err_word, stream)
     if status:
         _check("mla_cache_commit", status)
 

@@ -11,7 +11,10 @@
 
 namespace {
 
-PyObject* g_data_ptr = nullptr;   // "data_ptr"
+PyObject* g_data_ptr = nullptr;      // "data_ptr"
+PyObject* g_cuda_stream = nullptr;   // "cuda_stream"
+PyObject* g_device = nullptr;        // callables set by set_stream_getters: the current device,
+PyObject* g_raw_stream = nullptr;    // and a device's current stream as an integer
 
 // Reads the arguments of one call in order; `ok` goes false at the first bad
 // one, with the Python error set.
@@ -52,6 +55,28 @@ struct Reader {
     if (v == -1.0 && PyErr_Occurred()) ok = false;
     return (float)v;
   }
+  // None: the current stream of the current device
+  cudaStream_t stream() {
+    PyObject* a = args[at++];
+    if (!ok) return nullptr;
+    if (PyLong_Check(a)) return static_cast<cudaStream_t>(address(a));
+    PyObject* r = nullptr;
+    if (a != Py_None) {
+      r = PyObject_GetAttr(a, g_cuda_stream);
+    } else if (!g_raw_stream) {
+      PyErr_SetString(PyExc_RuntimeError, "no stream given and no current stream known");
+    } else if (PyObject* dev = PyObject_CallNoArgs(g_device)) {
+      r = PyObject_CallOneArg(g_raw_stream, dev);
+      Py_DECREF(dev);
+    }
+    if (!r) {
+      ok = false;
+      return nullptr;
+    }
+    auto st = static_cast<cudaStream_t>(address(r));
+    Py_DECREF(r);
+    return st;
+  }
   template <typename T>
   T* as() { return static_cast<T*>(ptr()); }
   mla_dtype dtype() { return static_cast<mla_dtype>(num()); }
@@ -86,7 +111,7 @@ MLA_ENTRY(step_plan, 23, {
   const int max_pages = r.num(), page = r.num(), num_pages = r.num();
   auto* row_start = r.as<int32_t>(); auto* kv_lens = r.as<int32_t>(); auto* seq_ids = r.as<int32_t>();
   auto* positions = r.as<int32_t>(); auto* slots = r.as<int32_t>(); auto* mask = r.as<uint64_t>();
-  auto* err = r.as<int32_t>(); auto stream = static_cast<cudaStream_t>(r.ptr());
+  auto* err = r.as<int32_t>(); auto stream = r.stream();
   MLA_CALL(mla_step_plan(lens, counts, parents, batch, max_rows, words, held_in, held_out, free_pages, fc_in, fc_out,
                          table, max_pages, page, num_pages, row_start, kv_lens, seq_ids, positions, slots, mask, err,
                          stream))
@@ -99,7 +124,7 @@ MLA_ENTRY(cache_append_slots, 16, {
   auto* cos = r.as<const float>(); auto* sin = r.as<const float>(); const int max_pos = r.num();
   auto* cache = r.as<void>(); auto* scale = r.as<float>(); const mla_dtype dtype = r.dtype();
   const int num_pages = r.num();
-  auto* err = r.as<int32_t>(); auto stream = static_cast<cudaStream_t>(r.ptr());
+  auto* err = r.as<int32_t>(); auto stream = r.stream();
   MLA_CALL(mla_cache_append_slots(kv, kv_dtype, n, slots, positions, gain, eps, cos, sin, max_pos, cache, scale,
                                   dtype, num_pages, err, stream))
 })
@@ -113,7 +138,7 @@ MLA_ENTRY(decode_tree, 23, {
   const int batch = r.num(), max_rows = r.num(), heads = r.num();
   auto* mask = r.as<const uint64_t>(); const int words = r.num(); const float softmax_scale = r.real();
   auto* ws = r.as<void>(); auto* o = r.as<void>(); const mla_dtype o_dtype = r.dtype(); auto* lse = r.as<float>();
-  auto* err = r.as<int32_t>(); auto stream = static_cast<cudaStream_t>(r.ptr());
+  auto* err = r.as<int32_t>(); auto stream = r.stream();
   MLA_CALL(mla_decode_tree(q, q_dtype, cache, scale, dtype, num_pages, table, max_pages, page, kv_lens, row_start,
                            batch, max_rows, heads, mask, words, softmax_scale, ws, o, o_dtype, lse, err, stream))
 })
@@ -125,14 +150,24 @@ MLA_ENTRY(cache_commit, 16, {
   auto* table = r.as<const int32_t>(); const int max_pages = r.num(), page = r.num();
   auto* cache = r.as<void>(); auto* scale = r.as<float>(); const mla_dtype dtype = r.dtype();
   const int num_pages = r.num();
-  auto* lens_out = r.as<int32_t>(); auto* err = r.as<int32_t>(); auto stream = static_cast<cudaStream_t>(r.ptr());
+  auto* lens_out = r.as<int32_t>(); auto* err = r.as<int32_t>(); auto stream = r.stream();
   MLA_CALL(mla_cache_commit(kv_lens, row_start, batch, max_rows, counts, nodes, table, max_pages, page, cache, scale,
                             dtype, num_pages, lens_out, err, stream))
 })
 
+PyObject* set_stream_getters(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != 2) {
+    PyErr_SetString(PyExc_TypeError, "set_stream_getters takes two callables");
+    return nullptr;
+  }
+  Py_XSETREF(g_device, Py_NewRef(args[0]));
+  Py_XSETREF(g_raw_stream, Py_NewRef(args[1]));
+  Py_RETURN_NONE;
+}
+
 #define MLA_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {MLA_METHOD(step_plan), MLA_METHOD(cache_append_slots), MLA_METHOD(decode_tree),
-                           MLA_METHOD(cache_commit), {nullptr, nullptr, 0, nullptr}};
+                           MLA_METHOD(cache_commit), MLA_METHOD(set_stream_getters), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_native", "Fast argument marshalling for libmla.so.", -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};
 
@@ -140,5 +175,6 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_native", "Fast argument marshal
 
 PyMODINIT_FUNC PyInit__native() {
   g_data_ptr = PyUnicode_InternFromString("data_ptr");
-  return g_data_ptr ? PyModule_Create(&g_module) : nullptr;
+  g_cuda_stream = PyUnicode_InternFromString("cuda_stream");
+  return g_data_ptr && g_cuda_stream ? PyModule_Create(&g_module) : nullptr;
 }
