@@ -76,6 +76,12 @@ constexpr float kRescaleLog2 = 8.0f;      // lazy rescale threshold (log2 units)
 constexpr float kRescaleLog2Q8 = 4.0f;    // 8-bit MMAs: probabilities stay <= 2^4, and times
 constexpr float kPScale8 = 16.0f;         // 16 x row scale / reference <= 16 x 1.75 ...
 constexpr float kScaleSlack8 = 1.75f;     // ... the reference is raised past 1.75x: <= 448
+// What cutting row tiles costs a call whose pairs are all busy, in tiles of a
+// pair: a second segment, the partials and their merge.  128 sequences of one
+// row tile of two tiles: 49.6 us cut evenly, 34.5 whole; 60 of sixteen: 93 and
+// 86; 4 of up to three, most pairs idle: 17.8 cut and 20.1 whole, hence the
+// rule only where there is more than a tile for every pair.
+constexpr int kSplitTiles = 3;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;             // S of tile t at kColS + 128 (t & 1)
 constexpr uint32_t kColO = 256;           // O: dims 0..255 at 256, dims 256..511 at 384
@@ -310,7 +316,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     used = min(n_pairs, total);
     g0 = pair < used ? (int)((long long)pair * total / used) : total;
     g1 = pair < used ? (int)((long long)(pair + 1) * total / used) : total;
-    const bool dealt = row_tiles > n_pairs && row_tiles <= 64 * n_pairs && p.batch <= kMaxDealt;
+    // (also with fewer row tiles than pairs, where whole ones may do: see below)
+    const int share = used ? (total + used - 1) / used : 0;
+    const bool whole = share > 1 && total <= (long long)(share + kSplitTiles) * row_tiles;
+    bool dealt = row_tiles <= 64 * n_pairs && p.batch <= kMaxDealt && (row_tiles > n_pairs || whole);
     stride = dealt ? n_pairs : 1;
     // part0: row tile index, cached tile within it, tiles to the end of its
     // column, its sequence, row tiles before that sequence
@@ -324,7 +333,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         before += q.rt;
       }
       __syncthreads();
-      if (warp == 0 && g0 < g1) {
+      // a column per pair, where the longest is not much longer than an even
+      // share: nothing is cut, so nothing is merged
+      const int longest = __reduce_max_sync(0xffffffffu, max(max(col[lane], col[lane + 32]), col[lane + 64]));
+      if (whole && longest <= share + kSplitTiles) {
+        g0 = 0;                                          // (positions matter to cut row tiles only)
+        g1 = col[pair];
+        if (threadIdx.x == 0) {
+          part0[0] = pair;
+          part0[1] = 0;
+          part0[2] = g1;
+        }
+      } else if (row_tiles <= n_pairs) {
+        dealt = false;
+        stride = 1;
+      } else if (warp == 0 && g0 < g1) {
         int at = 0, c = 0;                               // tiles before column c
         for (; g0 >= at + col[c]; ++c) at += col[c];
         const int end = at + col[c];
@@ -357,7 +380,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           at += __shfl_sync(0xffffffffu, upto, 31);
         }
       }
-    } else if (g0 < g1 && base.x <= g0 && g0 < base.x + sum.x) {
+    }
+    if (!dealt && g0 < g1 && base.x <= g0 && g0 < base.x + sum.x) {
       int b = b_lo;
       for (;; ++b) {
         const SeqInfo q = seq_info(p, b);

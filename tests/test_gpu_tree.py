@@ -158,6 +158,9 @@ CASES = [
     ("wide_tree", "bf16", 32, [130, 65], [33, 400], "random"),
     ("many_seqs", "bf16", 24, [1 + (7 * i) % 5 for i in range(400)], [(37 * i) % 300 for i in range(400)], "tree"),
     ("dealt_out", "bf16", 128, [1 + (5 * i) % 9 for i in range(30)], [(211 * i) % 1500 for i in range(30)], "tree"),
+    ("whole_columns", "bf16", 128, [1 + i % 2 for i in range(90)], [300 + (53 * i) % 200 for i in range(90)], "tree"),
+    ("whole_columns_fewer_rows", "e4m3", 128, [1 + i % 2 for i in range(40)], [300 + (53 * i) % 200 for i in range(40)],
+     "tree"),
     ("more_seqs_than_dealt", "bf16", 40, [1 + i % 2 for i in range(1100)], [(37 * i) % 300 for i in range(1100)],
      "chain"),
     ("split_tiles", "bf16", 128, [20, 20], [3000, 9000], "tree"),
