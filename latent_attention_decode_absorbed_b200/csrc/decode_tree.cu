@@ -21,10 +21,10 @@
 //
 // Work split.  The launch has one persistent CTA pair per SM pair and no
 // split count: the tiles (row tile x cached tile) of all sequences form one
-// list, in (sequence, row tile, cached tile) order, and pair p takes the p-th
-// equal part of it.  Each CTA finds its part by a scan over the sequences'
-// lengths at its start, so lengths stay on the device and a captured graph
-// serves any of them.  A row tile that one pair covers alone is normalised
+// list, a row tile's cached tiles next to each other, and pair p takes the
+// p-th equal part of it (or whole row tiles, where those balance).  Each CTA
+// finds its part by a scan over the sequences' lengths at its start, so lengths
+// stay on the device and a captured graph serves any of them.  A row tile that one pair covers alone is normalised
 // and stored as the final result; a row tile that crosses a pair's border
 // leaves at most two partials per pair (its first and its last segment) in
 // the workspace, which tree_merge_kernel joins.  The partials are thus
@@ -319,7 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // (also with fewer row tiles than pairs, where whole ones may do: see below)
     const int share = used ? (total + used - 1) / used : 0;
     const bool whole = share > 1 && total <= (long long)(share + kSplitTiles) * row_tiles;
-    bool dealt = row_tiles <= 64 * n_pairs && p.batch <= kMaxDealt && (row_tiles > n_pairs || whole);
+    bool dealt = n_pairs > 1 && row_tiles <= 64 * n_pairs && p.batch <= kMaxDealt && (row_tiles > n_pairs || whole);
     stride = dealt ? n_pairs : 1;
     // part0: row tile index, cached tile within it, tiles to the end of its
     // column, its sequence, row tiles before that sequence
@@ -528,7 +528,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         // rows outside the table or the pool read page 0 (readable; they are masked)
         auto page = [&](int pg) -> int { return pg >= 0 && pg < p.num_pages ? pg : 0; };
-        // the next stage: false where it is the other producer's (or the launch aborts)
+        // the next stage: false where it is the other producer's (or the launch
+        // aborts).  The slot's previous stage, n - kSlots, is the other
+        // producer's; its release is waited for, and the one before that cannot
+        // be outstanding (a parity wait would take the one for the other): this
+        // producer's last stage, n - 2, went to a slot freed by stage n - 2 -
+        // kSlots, and the MMAs free the slots in order.
         auto take = [&](uint32_t& dst, uint32_t& fb) -> bool {
           const uint32_t my = kc++;
           if ((int)(my % kProducers) != warp || !ok) return false;
