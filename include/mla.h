@@ -388,7 +388,8 @@ size_t mla_decode_tree_workspace_bytes(mla_dtype cache_dtype, int max_rows, int 
  *   q_abs       device [max_rows, n_heads, 576], q_dtype F32 or BF16
  *   cache, cache_scale, block_table  as for mla_decode_fwd (its pool contract too:
  *               rows of a visited page behind the sequence's end and drafted rows
- *               that a mask hides must hold finite values)
+ *               that a mask hides must hold finite values; over an F32 cache they may
+ *               hold anything)
  *   kv_lens     device int32 [batch];  row_start device int32 [batch + 1], ascending
  *               from row_start[0] >= 0 to at most max_rows.  A sequence whose numbers
  *               are impossible (L_b < n_b, L_b beyond its table row) is skipped and

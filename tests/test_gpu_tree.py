@@ -229,6 +229,29 @@ def test_rows_behind_the_end_do_not_count(cache):
     assert torch.equal(first, a.o)
 
 
+def test_f32_hidden_rows_may_hold_anything():
+    """NaN and infinities in rows that no node sees change no bit over an fp32 cache."""
+    p = Problem("f32", 20, [6, 3], [100, 30], "tree", seed=17)
+    for b in range(2):                                 # the last drafted row is seen by nobody
+        n, s = p.counts[b], p.seen[b]
+        s[:, n - 1] = False
+        p.mask[int(p.start[b]):int(p.start[b]) + n, 0] = _dev(pack_mask(s, 1))[:, 0]
+    p.run()
+    torch.cuda.synchronize()
+    first, lse = p.o.clone(), p.lse.clone()
+    rows = mla.unpack_cache_rows(p.pool).clone()
+    for b in range(2):
+        L = p.lens[b]
+        last = int(p.bt[b, (L - 1) // 64]) * 64
+        rows[last + (L - 1) % 64] = float("nan")
+        rows[last + (L - 1) % 64 + 1:last + 64] = float("inf")
+    p.pool.copy_(mla.pack_cache_rows(rows))
+    p.run()
+    torch.cuda.synchronize()
+    assert torch.equal(first, p.o) and torch.equal(lse, p.lse)
+    assert not bool(torch.isnan(p.o).any())
+
+
 def test_same_bits_again_and_on_another_stream():
     p = Problem("bf16", 128, [20, 7, 33], [3000, 500, 900], "tree", seed=9)
     p.run()
