@@ -529,11 +529,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // rows outside the table or the pool read page 0 (readable; they are masked)
         auto page = [&](int pg) -> int { return pg >= 0 && pg < p.num_pages ? pg : 0; };
         // the next stage: false where it is the other producer's (or the launch
-        // aborts).  The slot's previous stage, n - kSlots, is the other
-        // producer's; its release is waited for, and the one before that cannot
-        // be outstanding (a parity wait would take the one for the other): this
-        // producer's last stage, n - 2, went to a slot freed by stage n - 2 -
-        // kSlots, and the MMAs free the slots in order.
+        // aborts).  The slot's previous stage, n - kSlots, may be the other
+        // producer's (an odd ring); its release is waited for, and the one
+        // before that cannot be outstanding (a parity wait would take the one
+        // for the other): this producer's last stage, n - 2, went to a slot
+        // freed by stage n - 2 - kSlots, and the MMAs free the slots in order.
         auto take = [&](uint32_t& dst, uint32_t& fb) -> bool {
           const uint32_t my = kc++;
           if ((int)(my % kProducers) != warp || !ok) return false;
