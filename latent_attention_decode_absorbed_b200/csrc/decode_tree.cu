@@ -45,8 +45,8 @@
 // With an e4m3 cache both GEMMs run on kind::f8f6f4 straight from the cache
 // codes: the query as two e4m3 terms on a power-of-two scale (split_q_tree
 // below: exact for all but tiny components, so the scores are fp32-exact
-// products), the softmax weights as two e4m3 terms with the row scales
-// folded in relative to a running reference, as in decode_pair.cu.
+// products), the softmax weights as two e4m3 terms with the row scales folded
+// in, on a reference of their own per (node, head).
 #include <math.h>
 
 #include <type_traits>
@@ -73,9 +73,9 @@ constexpr int kProducers = 2;             // warps 0, 1: TMA producers
 constexpr int kWarpMma = kProducers, kWarpSoft0 = kWarpMma + 1, kSoftWarps = 8;
 constexpr int kThreads = 32 * (kWarpSoft0 + kSoftWarps);
 constexpr float kRescaleLog2 = 8.0f;      // lazy rescale threshold (log2 units)
-constexpr float kRescaleLog2Q8 = 4.0f;    // 8-bit MMAs: probabilities stay <= 2^4, and times
-constexpr float kPScale8 = 16.0f;         // 16 x row scale / reference <= 16 x 1.75 ...
-constexpr float kScaleSlack8 = 1.75f;     // ... the reference is raised past 1.75x: <= 448
+constexpr float kPLog8 = 4.0f;            // 8-bit MMAs: a weight at the reference is carried as 2^4,
+constexpr float kRescaleLog2Q8 = 4.8f;    // and the reference is raised past 4.8: at most 2^8.8 < 448
+constexpr float kLeastScale8 = 0x1p-48f;  // smaller row scales count as this one (see the softmax)
 // What cutting row tiles costs a call whose pairs are all busy, in tiles of a
 // pair: a second segment, the partials and their merge.  128 sequences of one
 // row tile of two tiles: 49.6 us cut evenly, 34.5 whole; 60 of sixteen: 93 and
@@ -92,14 +92,14 @@ constexpr int kMTmem = 64 * 8;
 constexpr int kMAbort = kMTmem + 4;
 constexpr int kMRedMax = kMTmem + 16;     // float [2 tile parities][4 parts][64 rows]
 constexpr int kMRedSum = kMRedMax + 2 * 4 * kHM * 4;    // float [4 parts][64 rows]
-constexpr int kMRedSc = kMRedSum + 4 * kHM * 4;         // float [2 tile parities][8 softmax warps]: 8-bit MMAs
 constexpr int kMaxPairs = 96;             // bound of the workspace's partials, whatever the GPU's SM count
 constexpr int kMaxDealt = 1024;           // sequences whose row tiles can be dealt out (their prefix sums are kept)
-constexpr int kMScan = kMRedSc + 4 * 2 * kSoftWarps;    // int2 [16]: per-warp sums of the schedule's scan
-constexpr int kMPart = kMScan + 8 * 16;                 // int [8]: where this pair's part begins (see there)
+constexpr int kMPart = kMRedSum + 4 * kHM * 4;          // int [8]: where this pair's part begins (see there)
 constexpr int kMCol = kMPart + 4 * 8;                   // int [96]: tiles of each column
-constexpr int kMRt = kMCol + 4 * kMaxPairs;             // int [1024]: row tiles before each sequence
-constexpr int kMiscBytes = kMRt + 4 * kMaxDealt;
+constexpr int kMRt = kMCol + 4 * kMaxPairs;             // uint16 [1024]: row tiles before each sequence
+constexpr int kMScale = kMRt + 2 * kMaxDealt;           // float [4][4 pages][64 rows]: 8-bit MMAs, see the softmax
+constexpr int kMScan = kMScale;                         // int2 [16]: per-warp sums of the schedule's scan, before that
+constexpr int kMiscBytes = kMScale + 4 * 4 * 4 * 64;
 
 template <bool D8>
 struct TreeLayout {
@@ -233,11 +233,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + kMAbort);
   float* red_max = reinterpret_cast<float*>(misc + kMRedMax);
   float* red_sum = reinterpret_cast<float*>(misc + kMRedSum);
-  float* red_sc = reinterpret_cast<float*>(misc + kMRedSc);
   int2* scan = reinterpret_cast<int2*>(misc + kMScan);
   int* part0 = reinterpret_cast<int*>(misc + kMPart);
   int* col = reinterpret_cast<int*>(misc + kMCol);
-  int* rt_before = reinterpret_cast<int*>(misc + kMRt);
+  uint16_t* rt_before = reinterpret_cast<uint16_t*>(misc + kMRt);   // at most 64 per pair, see `dealt`
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t lim = p.wait_limit;
@@ -327,7 +326,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int before = base.y;
       for (int b = b_lo; b < b_hi; ++b) {
         const SeqInfo q = seq_info(p, b);
-        rt_before[b] = before;
+        rt_before[b] = (uint16_t)before;
         for (int x = 0; x < min(q.rt, stride); ++x)      // q.rt row tiles over consecutive columns
           atomicAdd(col + (before + x) % stride, q.kt * ((q.rt - x + stride - 1) / stride));
         before += q.rt;
@@ -742,10 +741,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const size_t grow = (size_t)s.start * p.n_heads + my;   // ... of the whole call
       const int prefix = s.L - s.n;
       const uint64_t* mask = p.tree_mask ? p.tree_mask + (size_t)(s.start + node) * p.mask_words : nullptr;
-      float slq = p.scale_log2, s_ref = 0.f;
+      float slq = p.scale_log2;
       if constexpr (D8) {
         if (my < seq_rows) slq *= p.q_scale[grow];
       }
+      // D8.  The weight MMAs multiply codes, so a row's weight has to carry
+      // its scale: with y_j = z_j + log2 sc_j (z_j in log2 units) the weight
+      // operand is x_j = 16 * 2^(y_j - m), m a reference for the y's that only
+      // rows this thread's (node, head) sees can move.  The sum of the softmax
+      // takes the same x_j over sc_j, so O / sum is the result with no factor
+      // left.  Measured against the scores alone, with the scales relative to
+      // the largest one of the tile, a row of large scale and no weight, or one
+      // that the mask hides, pushed the others' weights below e4m3's last step.
+      // A page's scales, their logarithms and reciprocals wait in shared
+      // memory; scales below 2^-48 (rows below 2e-12) count as 2^-48, which
+      // keeps the sum finite.  Both warps of a page write the same values; the
+      // reciprocals, read after the tile's sync, alternate by tile.  Each read
+      // is issued four columns before its values are used (128 x 2-6 drafts x
+      // 128 heads over 2048-4096 rows: 458 us a call without that, 425 with it;
+      // two shuffles per column instead 430).
+      float* page_sc = reinterpret_cast<float*>(misc + kMScale) + part * 64;   // scales, logarithms, 2 x reciprocals
+      constexpr int kScalePlane = 4 * 64;
       float m_run = -INFINITY, l_acc = 0.f;
       for (int i = 0; i < s.nt; ++i) {
         const uint32_t t = gt + i;
@@ -767,6 +783,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         }
+        float* page_inv = page_sc + (2 + sb) * kScalePlane;
+        if constexpr (D8) {
+          const float a = fmaxf(sc_lo, kLeastScale8), c = fmaxf(sc_hi, kLeastScale8);
+          page_sc[lane] = sc_lo;
+          page_sc[lane + 32] = sc_hi;
+          page_sc[kScalePlane + lane] = log2f(a);
+          page_sc[kScalePlane + lane + 32] = log2f(c);
+          page_inv[lane] = 1.0f / a;
+          page_inv[lane + 32] = 1.0f / c;
+          __syncwarp();
+        }
         const bool full = __all_sync(0xffffffffu, vis == ~0ull);
         ok = __all_sync(0xffffffffu, mbar_wait<false>(bar(kBSFull + sb), (t >> 1) & 1, abort_flag, lim));
         if (!ok) break;
@@ -777,11 +804,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_ld<32>(scol + 64 * ch + 32, v + 32);
         tmem_wait_ld();
         float mx = -INFINITY;
+        if constexpr (D8) {
+          const uint32_t a_sc = smem_u32(page_sc);
+          float4 sc_n = ld_shared_f4(a_sc), lg_n = ld_shared_f4(a_sc + 4 * kScalePlane);
 #pragma unroll
-        for (int j = 0; j < 64; ++j) {
-          float sl = slq;
-          if constexpr (D8) sl *= __shfl_sync(0xffffffffu, j < 32 ? sc_lo : sc_hi, j & 31);
-          v[j] *= sl;
+          for (int j = 0; j < 64; j += 4) {
+            const float4 sc = sc_n, lg = lg_n;
+            if (j < 60) {
+              sc_n = ld_shared_f4(a_sc + 4 * (j + 4));
+              lg_n = ld_shared_f4(a_sc + 4 * (kScalePlane + j + 4));
+            }
+            v[j] = fmaf(v[j] * slq, sc.x, lg.x);
+            v[j + 1] = fmaf(v[j + 1] * slq, sc.y, lg.y);
+            v[j + 2] = fmaf(v[j + 2] * slq, sc.z, lg.z);
+            v[j + 3] = fmaf(v[j + 3] * slq, sc.w, lg.w);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 64; ++j) v[j] *= slq;
         }
         if (!full) {
           const uint32_t vlo = (uint32_t)vis, vhi = (uint32_t)(vis >> 32);
@@ -796,12 +836,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // sync, so no warp can overwrite a slot that another is still reading
         float* rm = red_max + sb * 4 * kHM;
         rm[part * kHM + hh] = mx;
-        if constexpr (D8) {   // the largest scale of this warp's rows, same buffering
-          float tsm = fmaxf(sc_lo, sc_hi);
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) tsm = fmaxf(tsm, __shfl_xor_sync(0xffffffffu, tsm, o));
-          if (lane == 0) red_sc[sb * kSoftWarps + (warp - kWarpSoft0)] = tsm;
-        }
         if (!(ok = soft_sync())) break;
         const float tmax = fmaxf(fmaxf(rm[hh], rm[kHM + hh]), fmaxf(rm[2 * kHM + hh], rm[3 * kHM + hh]));
         const float m_new = (tmax > m_run + (D8 ? kRescaleLog2Q8 : kRescaleLog2)) ? tmax : m_run;
@@ -809,41 +843,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // factor for the sums and the accumulator kept so far (0 when nothing was kept)
         const float alpha = (m_run == -INFINITY) ? 0.f : exp2_approx(m_run - m_new);
         m_run = m_new;
-        const float msub = m_new == -INFINITY ? 0.f : m_new;
-        float w_k = 0.f, s_fac = 1.f;   // D8: weight factor 16 / s_ref; O's factor for a raised s_ref
-        bool s_up = false;
-        if constexpr (D8) {
-          const float* rs = red_sc + sb * kSoftWarps;
-          float tsmax = rs[0];
-#pragma unroll
-          for (int x = 1; x < kSoftWarps; ++x) tsmax = fmaxf(tsmax, rs[x]);
-          if (tsmax > kScaleSlack8 * s_ref) {
-            s_up = s_ref > 0.f;
-            s_fac = s_up ? s_ref / tsmax : 1.f;
-            s_ref = tsmax;
-          }
-          w_k = s_ref > 0.f ? kPScale8 / s_ref : 0.f;
-        }
+        const float msub = m_new == -INFINITY ? 0.f : (D8 ? m_new - kPLog8 : m_new);
         uint32_t pk[32];   // D8: pk[0..15] the hi codes of the 64 rows, pk[16..31] the lo codes
         float sum = 0.f;
         if constexpr (D8) {
-          const float wlo = sc_lo * w_k, whi = sc_hi * w_k;
+          float sum2 = 0.f;
+          const uint32_t a_inv = smem_u32(page_inv);
+          float4 inv_n = ld_shared_f4(a_inv);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float p0 = exp2_approx(v[2 * j] - msub), p1 = exp2_approx(v[2 * j + 1] - msub);
-            sum += p0 + p1;
-            const float x0 = p0 * __shfl_sync(0xffffffffu, 2 * j < 32 ? wlo : whi, (2 * j) & 31);
-            const float x1 = p1 * __shfl_sync(0xffffffffu, 2 * j + 1 < 32 ? wlo : whi, (2 * j + 1) & 31);
-            uint32_t h2, l2;
-            split_e4m3x2(x0, x1, h2, l2);
-            if (j & 1) {
-              pk[j >> 1] |= h2 << 16;
-              pk[16 + (j >> 1)] |= l2 << 16;
-            } else {
-              pk[j >> 1] = h2;
-              pk[16 + (j >> 1)] = l2;
-            }
+          for (int j = 0; j < 64; j += 4) {
+            const float4 inv = inv_n;
+            if (j < 60) inv_n = ld_shared_f4(a_inv + 4 * (j + 4));
+            const float x0 = exp2_approx(v[j] - msub), x1 = exp2_approx(v[j + 1] - msub);
+            const float x2 = exp2_approx(v[j + 2] - msub), x3 = exp2_approx(v[j + 3] - msub);
+            sum = fmaf(x1, inv.y, fmaf(x0, inv.x, sum));
+            sum2 = fmaf(x3, inv.w, fmaf(x2, inv.z, sum2));
+            uint32_t h01, l01, h23, l23;
+            split_e4m3x2(x0, x1, h01, l01);
+            split_e4m3x2(x2, x3, h23, l23);
+            pk[j >> 2] = h01 | h23 << 16;
+            pk[16 + (j >> 2)] = l01 | l23 << 16;
           }
+          sum += sum2;
         } else {
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
@@ -860,8 +881,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = __all_sync(0xffffffffu, mbar_wait<false>(bar(kBODone), (t - 1) & 1, abort_flag, lim));
           if (!ok) break;
           tc_fence_after();
-          if (s_up || __any_sync(0xffffffffu, changed)) {
-            const float f = (changed ? alpha : 1.f) * s_fac;
+          if (__any_sync(0xffffffffu, changed)) {
+            const float f = changed ? alpha : 1.f;
             const uint32_t oc = tmem + lane_addr + kColO + 128 * ch;
 #pragma unroll 1
             for (int c4 = 0; c4 < 4; ++c4) {
@@ -907,12 +928,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (ok) {
         const float lt = red_sum[hh] + red_sum[kHM + hh] + red_sum[2 * kHM + hh] + red_sum[3 * kHM + hh];
-        const float inv_l = lt > 0.f ? (D8 ? s_ref / kPScale8 : 1.f) / lt : 0.f;
+        const float inv_l = lt > 0.f ? 1.f / lt : 0.f;
         const bool whole = s.nt == s.kt;
         // a first segment that continues a row tile: slot 2 pair; a last one that leaves its row tile open: 2 pair + 1
         const int slot = 2 * pair + (s.k0 == 0 ? 1 : 0);
         if (part == 0) {
-          const float lv = lt > 0.f ? (m_run + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+          const float lv = lt > 0.f ? (m_run - (D8 ? kPLog8 : 0.f) + log2f(lt)) * 0.69314718055994531f : -INFINITY;
           if (!whole) p.part_lse[slot * kM + kHM * (int)rank + hh] = lv;
           else if (p.lse && my < seq_rows) p.lse[grow] = lv;
         }
