@@ -407,8 +407,11 @@ size_t mla_decode_tree_workspace_bytes(mla_dtype cache_dtype, int max_rows, int 
  * Rows of o_lat and lse_out that belong to no sequence are left as they were.
  * Supported: page_size 64; q F32 with cache F32 (CUDA cores), q BF16 with cache
  * BF16 or E4M3 (tcgen05 tensor cores, fp32 accumulation).  The softmax weights
- * enter the value product as bf16 (BF16 cache) or as two e4m3 terms (E4M3
- * cache, whose queries must be finite); scores, sums and statistics are fp32.
+ * enter the value product as bf16 (BF16 cache) or, times their row's scale, as an
+ * e4m3 and an e5m2 term (E4M3 cache, whose queries must be finite): to 2^-8 of
+ * themselves or 2^-18 of a reference that is at most 2^8 times the largest weight
+ * among the same 256 rows; row scales below 2^-48 count as 2^-48.  Scores, sums
+ * and statistics are fp32.
  * Results do not depend on timing: a call on the same inputs and GPU returns
  * the same bits.  Calls that share a workspace must not overlap on the GPU, so
  * two captured graphs that may replay at once need a workspace each.

@@ -45,8 +45,8 @@
 // With an e4m3 cache both GEMMs run on kind::f8f6f4 straight from the cache
 // codes: the query as two e4m3 terms on a power-of-two scale (split_q_tree
 // below: exact for all but tiny components, so the scores are fp32-exact
-// products), the softmax weights as two e4m3 terms with the row scales folded
-// in, on a reference of their own per (node, head).
+// products), the softmax weights as an e4m3 and an e5m2 term with the row
+// scales folded in, on a reference of their own per (node, head).
 #include <math.h>
 
 #include <type_traits>
@@ -74,7 +74,9 @@ constexpr int kWarpMma = kProducers, kWarpSoft0 = kWarpMma + 1, kSoftWarps = 8;
 constexpr int kThreads = 32 * (kWarpSoft0 + kSoftWarps);
 constexpr float kRescaleLog2 = 8.0f;      // lazy rescale threshold (log2 units)
 constexpr float kPLog8 = 4.0f;            // 8-bit MMAs: a weight at the reference is carried as 2^4,
-constexpr float kRescaleLog2Q8 = 4.8f;    // and the reference is raised past 4.8: at most 2^8.8 < 448
+constexpr float kRescaleLog2Q8 = 4.8f;    // the reference is raised past 4.8 (at most 2^8.8 < 448) ...
+constexpr float kLowerLog2Q8 = 8.0f;      // ... and lowered to a tile whose largest is more than 8 below it, ...
+constexpr float kLowestLog2Q8 = 32.0f;    // ... to 32 below the largest so far at most
 constexpr float kLeastScale8 = 0x1p-48f;  // smaller row scales count as this one (see the softmax)
 // What cutting row tiles costs a call whose pairs are all busy, in tiles of a
 // pair: a second segment, the partials and their merge.  128 sequences of one
@@ -591,6 +593,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (leader) {
       constexpr uint32_t idS = D8 ? idesc_e4m3(kM, 256, false, false) : idesc_f16(kM, 256, false, false);
       constexpr uint32_t idO = D8 ? idesc_e4m3(kM, 256, false, true) : idesc_f16(kM, 256, false, true);
+      constexpr uint32_t idO_lo = idesc_e4m3(kM, 256, false, true, true);    // D8: the weights' second term is e5m2
       // Stages are taken in groups (three score chunks, a page's two value
       // boxes), whose barriers are waited for together.  The tensor cores hold
       // little more than one MMA in advance, so whatever stands between a
@@ -688,7 +691,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                   for (int hl = 0; hl < 2; ++hl)
                     mma_pair_e4m3_w(tmem + kColO + 128 * bb, pd + ((hl * kBox8 + ks * 32) >> 4),
-                                    vd + ((ks * 2048) >> 4), idO, (j | pg_i | ks | hl) != 0);
+                                    vd + ((ks * 2048) >> 4), hl ? idO_lo : idO, (j | pg_i | ks | hl) != 0);
               } else {
                 const uint64_t pd = smem_desc_sw128(s_p + pg_i * kPChunk, 16, 1024);
                 const uint64_t vd = smem_desc_sw128(b0, kBox, 1024);
@@ -753,6 +756,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // left.  Measured against the scores alone, with the scales relative to
       // the largest one of the tile, a row of large scale and no weight, or one
       // that the mask hides, pushed the others' weights below e4m3's last step.
+      // x_j is carried as e4m3(x) + e5m2(x - e4m3(x)): 2^-8 of itself down to
+      // 2^-6, 2^-14 below, so weights to about 2^-21 of the reference count.  m
+      // follows a tile down as well as up (O and the sum are fp32 and take any
+      // factor), so a long thin tail behind one strong row is carried on its
+      // own reference.  With two e4m3 terms and m only rising, weights under
+      // 2^-14 of the strongest were lost but stayed in the sum: with 0.3 to 0.9 of
+      // the mass on the first of 32768 rows o was off by 0.09 to 3.2 of its norm
+      // (now 3e-4 at most; 4096 to 131072 rows: 7e-4).
       // A page's scales, their logarithms and reciprocals wait in shared
       // memory; scales below 2^-48 (rows below 2e-12) count as 2^-48, which
       // keeps the sum finite.  Both warps of a page write the same values; the
@@ -762,7 +773,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // two shuffles per column instead 430).
       float* page_sc = reinterpret_cast<float*>(misc + kMScale) + part * 64;   // scales, logarithms, 2 x reciprocals
       constexpr int kScalePlane = 4 * 64;
-      float m_run = -INFINITY, l_acc = 0.f;
+      float m_run = -INFINITY, m_top = -INFINITY, l_acc = 0.f;
       for (int i = 0; i < s.nt; ++i) {
         const uint32_t t = gt + i;
         const uint32_t sb = t & 1u;
@@ -838,7 +849,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         rm[part * kHM + hh] = mx;
         if (!(ok = soft_sync())) break;
         const float tmax = fmaxf(fmaxf(rm[hh], rm[kHM + hh]), fmaxf(rm[2 * kHM + hh], rm[3 * kHM + hh]));
-        const float m_new = (tmax > m_run + (D8 ? kRescaleLog2Q8 : kRescaleLog2)) ? tmax : m_run;
+        float m_new = (tmax > m_run + (D8 ? kRescaleLog2Q8 : kRescaleLog2)) ? tmax : m_run;
+        if constexpr (D8) {
+          m_top = fmaxf(m_top, tmax);
+          if (tmax < m_run - kLowerLog2Q8 && tmax > -INFINITY) m_new = fmaxf(tmax, m_top - kLowestLog2Q8);
+        }
         const bool changed = m_new != m_run;
         // factor for the sums and the accumulator kept so far (0 when nothing was kept)
         const float alpha = (m_run == -INFINITY) ? 0.f : exp2_approx(m_run - m_new);
@@ -859,8 +874,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             sum = fmaf(x1, inv.y, fmaf(x0, inv.x, sum));
             sum2 = fmaf(x3, inv.w, fmaf(x2, inv.z, sum2));
             uint32_t h01, l01, h23, l23;
-            split_e4m3x2(x0, x1, h01, l01);
-            split_e4m3x2(x2, x3, h23, l23);
+            split_e4m3_e5m2x2(x0, x1, h01, l01);
+            split_e4m3_e5m2x2(x2, x3, h23, l23);
             pk[j >> 2] = h01 | h23 << 16;
             pk[16 + (j >> 2)] = l01 | l23 << 16;
           }

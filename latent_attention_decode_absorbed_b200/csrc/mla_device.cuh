@@ -100,4 +100,18 @@ __device__ __forceinline__ void split_e4m3x2(float x0, float x1, uint32_t& hi, u
   lo = l;
 }
 
+// The same with lo = e5m2(x - hi).  hi is off by half a step of e4m3 (x in
+// [2^k, 2^(k+1)): 2^(k-4), below 2^-6: 2^-10) and lo by half a step of its own:
+// together 2^(k-8), below 2^-6 at most 2^-14 or x / 8, and 2^-17 at e5m2's last
+// step.  lo as e4m3 halves the error of large x, but its last step is 2^-9 as
+// hi's is: x below 2^-10 is lost.
+__device__ __forceinline__ void split_e4m3_e5m2x2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+  const float2 b = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+  const __nv_fp8x2_storage_t l =
+      __nv_cvt_float2_to_fp8x2(make_float2(x0 - b.x, x1 - b.y), __NV_SATFINITE, __NV_E5M2);
+  hi = h;
+  lo = l;
+}
+
 }  // namespace mla

@@ -411,11 +411,13 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn_major, 
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// Instruction descriptor for kind::f8f6f4 with e4m3 A and B (format code 0)
-// and fp32 D; MN-major is allowed for e4m3 operands.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn_major, bool b_mn_major) {
+// Instruction descriptor for kind::f8f6f4 with e4m3 (format code 0) or e5m2
+// (1) A, e4m3 B and fp32 D; the kind's A and B formats are independent, and
+// MN-major is allowed for 8-bit operands.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn_major, bool b_mn_major,
+                                                  bool a_e5m2 = false) {
   return (1u << 4)                                   // D format: f32
-         | (0u << 7) | (0u << 10)                    // A, B format: e4m3
+         | ((a_e5m2 ? 1u : 0u) << 7) | (0u << 10)    // A, B format
          | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
