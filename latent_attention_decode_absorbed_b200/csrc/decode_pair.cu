@@ -8,8 +8,8 @@
 //   D8: e4m3 cache with the query in two e4m3 terms (hi + lo on one scale
 //       per head): both GEMMs on kind::f8f6f4 straight from the cache codes,
 //       64-byte swizzled stages of half the size (twice as many), the
-//       softmax weights written as two e4m3 terms with each row's scale
-//       folded in relative to a running reference.
+//       softmax weights written as an e4m3 and an e5m2 term with each row's
+//       scale folded in, on a running reference per head (softmax_q8.cuh).
 //
 // What it computes ("DeepSeek-V2: MLA Explained", "MLA Full Formulas" part 3
 // with the absorption of "Optimization Note"): for each head h of query row
@@ -67,6 +67,7 @@
 #include "mla_device.cuh"
 #include "mla_internal.h"
 #include "sm100.cuh"
+#include "softmax_q8.cuh"
 
 namespace mla {
 namespace {
@@ -88,9 +89,6 @@ constexpr int kWarpProd = 0, kWarpMma = 1, kWarpSoft0 = 2, kSoftWarps = 8;
 constexpr int kWarpConv0 = kWarpSoft0 + kSoftWarps, kConvWarps = 4;   // e4m3 cache: converters
 constexpr int kQN = 8;                    // unit queue depth
 constexpr float kRescaleLog2 = 8.0f;      // lazy rescale threshold (log2 units)
-constexpr float kRescaleLog2Q8 = 4.0f;    // 8-bit MMAs: probabilities stay <= 2^4, and times
-constexpr float kPScale8 = 16.0f;         // 16 x row scale / reference <= 16 x 1.75 ...
-constexpr float kScaleSlack8 = 1.75f;     // ... the reference is raised past 1.75x: <= 448
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;             // S of tile t at kColS + 128 (t & 1)
 constexpr uint32_t kColO = 256;           // O: dims 0..255 at 256, dims 256..511 at 384
@@ -103,8 +101,9 @@ constexpr int kMRedMax = kMTmem + 16;     // float [2 tile parities][2 lane halv
 constexpr int kMRedSum = kMRedMax + 2 * 4 * kHPC * 4;   // float [2 lane halves][2 column halves][64 heads]
 constexpr int kMUnitQ = kMRedSum + 4 * kHPC * 4;
 constexpr int kMStgSeq = kMUnitQ + 4 * kQN;   // int [8]: e4m3, the stage each staging slot was last filled for
-constexpr int kMRedSc = kMStgSeq + 4 * 8;    // float [2 tile parities][8 softmax warps]: 8-bit MMAs
-constexpr int kMiscBytes = kMRedSc + 4 * 2 * kSoftWarps;
+constexpr int kMScale = kMStgSeq + 4 * 8;    // 8-bit MMAs: the row scales of the four pages, see softmax_q8.cuh
+constexpr int kMiscBytes = kMScale + q8::kBytes;
+static_assert(kMScale % 16 == 0, "read as float4");
 
 // Shared memory, barriers and threads of the bf16 (F8 = D8 = false), the
 // widening e4m3 (F8) and the 8-bit MMA e4m3 (D8) kernels.  With F8 the
@@ -225,7 +224,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairLayout<F8, D8>::
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + kMAbort);
   float* red_max = reinterpret_cast<float*>(misc + kMRedMax);
   float* red_sum = reinterpret_cast<float*>(misc + kMRedSum);
-  float* red_sc = reinterpret_cast<float*>(misc + kMRedSc);
   int* unit_q = reinterpret_cast<int*>(misc + kMUnitQ);
   uint8_t* s_pbuf = smem + kOffP;
   const uint32_t s_p = s_base + kOffP;
@@ -499,6 +497,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairLayout<F8, D8>::
       // F8: the operands are f16 (widened codes, Q and P in f16); D8: e4m3
       constexpr uint32_t idS = D8 ? idesc_e4m3(128, 256, false, false) : idesc_f16(128, 256, false, false, F8);
       constexpr uint32_t idO = D8 ? idesc_e4m3(128, 256, false, true) : idesc_f16(128, 256, false, true, F8);
+      constexpr uint32_t idO_lo = idesc_e4m3(128, 256, false, true, true);   // D8: the weights' second term is e5m2
       auto ready = [&](uint32_t& src, uint32_t& empty) -> bool {
         const uint32_t slot = kc % kSlots;
         const uint32_t ph = (kc / kSlots) & 1u;
@@ -581,7 +580,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairLayout<F8, D8>::
 #pragma unroll
                   for (int hl = 0; hl < 2; ++hl)
                     mma_pair_e4m3_w(tmem + kColO + 128 * bb, pd + ((pg_i * kPChunk + hl * kBox8 + ks * 32) >> 4),
-                                    vd + ((ks * 2048) >> 4), idO, (j | pg_i | ks | hl) != 0);
+                                    vd + ((ks * 2048) >> 4), hl ? idO_lo : idO, (j | pg_i | ks | hl) != 0);
               } else {
                 const uint64_t pd = smem_desc_sw128(s_p, 16, 1024);
                 const uint64_t vd = smem_desc_sw128(b0, kBox, 1024);
@@ -648,17 +647,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairLayout<F8, D8>::
         if (part == 0 && head < p.n_heads) p.lse_part[((size_t)r * p.n_heads + head) * S + s] = -INFINITY;
         continue;
       }
-      // D8: the scores are (q scale of the head) x (row scale) x the code
-      // GEMM.  The weights of the value GEMM carry each row's scale relative
-      // to a reference s_ref, times 16: s_ref is the largest row scale seen so
-      // far in the segment, raised (with O rescaled) only when a tile's rows
-      // exceed it by 1.75x, so every weight stays <= 16 x 16 x 1.75 = 448.
-      // O is multiplied by s_ref / 16 in the epilogue.
-      float slq = p.scale_log2, s_ref = 0.f;
+      // D8: the scores are (q scale of the head) x (row scale) x the code GEMM
+      float slq = p.scale_log2;
       if constexpr (D8) {
         if (head < p.n_heads) slq *= __ldg(p.q_scale + (size_t)r * p.n_heads + head);
       }
-      float m_run = -INFINITY, l_acc = 0.f;
+      float* page_sc = reinterpret_cast<float*>(misc + kMScale) + part * 64;
+      float m_run = -INFINITY, m_top = -INFINITY, l_acc = 0.f;
       for (int i = 0; i < n_tiles; ++i) {
         const uint32_t t = gt + i;
         const uint32_t sb = t & 1u;
@@ -678,6 +673,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairLayout<F8, D8>::
             sc_hi = __ldg(p.cache_scale + (size_t)pg * 64 + 32 + lane);
           }
         }
+        float* page_inv = page_sc + (2 + sb) * q8::kPlane;
+        if constexpr (D8)
+          q8::put_scales(page_sc, page_inv, lane, lane < nvalid ? sc_lo : 0.f, lane + 32 < nvalid ? sc_hi : 0.f);
         ok = __all_sync(0xffffffffu, mbar_wait<false>(bar(kBSFull + sb), (t >> 1) & 1, abort_flag, lim));
         if (!ok) break;
         tc_fence_after();
@@ -687,10 +685,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairLayout<F8, D8>::
         tmem_ld<32>(scol + 64 * ch + 32, v + 32);
         tmem_wait_ld();
         float mx = -INFINITY;
+        if constexpr (D8) q8::scores(v, slq, page_sc);
 #pragma unroll
         for (int j = 0; j < 64; ++j) {
-          float sl = slq;
-          if constexpr (F8 || D8) sl *= __shfl_sync(0xffffffffu, j < 32 ? sc_lo : sc_hi, j & 31);
+          float sl = D8 ? 1.f : slq;
+          if constexpr (F8) sl *= __shfl_sync(0xffffffffu, j < 32 ? sc_lo : sc_hi, j & 31);
           v[j] = j < nvalid ? v[j] * sl : -INFINITY;
           mx = fmaxf(mx, v[j]);
         }
@@ -699,55 +698,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairLayout<F8, D8>::
         // sync, so no warp can overwrite a slot that another is still reading
         float* rm = red_max + sb * 4 * kHPC;
         rm[part * kHPC + hh] = mx;
-        if constexpr (D8) {   // the largest scale of this warp's visible rows, same buffering
-          float tsm = fmaxf(lane < nvalid ? sc_lo : 0.f, lane + 32 < nvalid ? sc_hi : 0.f);
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) tsm = fmaxf(tsm, __shfl_xor_sync(0xffffffffu, tsm, o));
-          if (lane == 0) red_sc[sb * kSoftWarps + (warp - kWarpSoft0)] = tsm;
-        }
         if (!(ok = soft_sync(0))) break;
         const float tmax = fmaxf(fmaxf(rm[hh], rm[kHPC + hh]), fmaxf(rm[2 * kHPC + hh], rm[3 * kHPC + hh]));
-        const float m_new = (tmax > m_run + (D8 ? kRescaleLog2Q8 : kRescaleLog2)) ? tmax : m_run;
+        float m_new;
+        if constexpr (D8) m_new = q8::reference(m_run, tmax, m_top);
+        else m_new = tmax > m_run + kRescaleLog2 ? tmax : m_run;
         const bool changed = m_new != m_run;
         // factor for the sums and the accumulator kept so far (0 when nothing was kept)
         const float alpha = (m_run == -INFINITY) ? 0.f : exp2_approx(m_run - m_new);
         m_run = m_new;
-        const float msub = m_new == -INFINITY ? 0.f : m_new;
-        float w_k = 0.f, s_fac = 1.f;   // D8: weight factor 16 / s_ref; O's factor for a raised s_ref
-        bool s_up = false;
-        if constexpr (D8) {
-          const float* rs = red_sc + sb * kSoftWarps;
-          float tsmax = rs[0];
-#pragma unroll
-          for (int w = 1; w < kSoftWarps; ++w) tsmax = fmaxf(tsmax, rs[w]);
-          if (tsmax > kScaleSlack8 * s_ref) {
-            s_up = s_ref > 0.f;
-            s_fac = s_up ? s_ref / tsmax : 1.f;
-            s_ref = tsmax;
-          }
-          w_k = s_ref > 0.f ? kPScale8 / s_ref : 0.f;
-        }
         uint32_t pk[32];   // D8: pk[0..15] the hi codes of the 64 rows, pk[16..31] the lo codes
         float sum = 0.f;
         if constexpr (D8) {
-          const float wlo = sc_lo * w_k, whi = sc_hi * w_k;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float p0 = exp2_approx(v[2 * j] - msub), p1 = exp2_approx(v[2 * j + 1] - msub);
-            sum += p0 + p1;
-            const float x0 = p0 * __shfl_sync(0xffffffffu, 2 * j < 32 ? wlo : whi, (2 * j) & 31);
-            const float x1 = p1 * __shfl_sync(0xffffffffu, 2 * j + 1 < 32 ? wlo : whi, (2 * j + 1) & 31);
-            uint32_t h2, l2;
-            split_e4m3x2(x0, x1, h2, l2);
-            if (j & 1) {
-              pk[j >> 1] |= h2 << 16;
-              pk[16 + (j >> 1)] |= l2 << 16;
-            } else {
-              pk[j >> 1] = h2;
-              pk[16 + (j >> 1)] = l2;
-            }
-          }
+          sum = q8::weights(v, m_new, page_inv, pk);
         } else {
+          const float msub = m_new == -INFINITY ? 0.f : m_new;
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             const float p0 = exp2_approx(v[2 * j] - msub), p1 = exp2_approx(v[2 * j + 1] - msub);
@@ -763,8 +728,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairLayout<F8, D8>::
           ok = __all_sync(0xffffffffu, mbar_wait<false>(bar(kBODone), (t - 1) & 1, abort_flag, lim));
           if (!ok) break;
           tc_fence_after();
-          if (s_up || __any_sync(0xffffffffu, changed)) {
-            const float f = (changed ? alpha : 1.f) * s_fac;
+          if (__any_sync(0xffffffffu, changed)) {
+            const float f = changed ? alpha : 1.f;
             const uint32_t oc = tmem + lane_addr + kColO + 128 * ch;
 #pragma unroll 1
             for (int c4 = 0; c4 < 4; ++c4) {
@@ -812,10 +777,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairLayout<F8, D8>::
       }
       if (ok) {
         const float lt = red_sum[hh] + red_sum[kHPC + hh] + red_sum[2 * kHPC + hh] + red_sum[3 * kHPC + hh];
-        const float inv_l = lt > 0.f ? (D8 ? s_ref / kPScale8 : 1.f) / lt : 0.f;
+        const float inv_l = lt > 0.f ? 1.f / lt : 0.f;
         if (part == 0 && head < p.n_heads)
           p.lse_part[((size_t)r * p.n_heads + head) * S + s] =
-              lt > 0.f ? (m_run + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+              lt > 0.f ? (m_run - (D8 ? q8::kLog : 0.f) + log2f(lt)) * 0.69314718055994531f : -INFINITY;
         // this thread's O: dims 256 ch + 128 half + (0..127) of head `head`,
         // stored 32 dims at a time through a 4 KB [32 heads x 32 dims] tile
         // of this warp in the P area (idle until the next unit's first

@@ -46,7 +46,7 @@
 // codes: the query as two e4m3 terms on a power-of-two scale (split_q_tree
 // below: exact for all but tiny components, so the scores are fp32-exact
 // products), the softmax weights as an e4m3 and an e5m2 term with the row
-// scales folded in, on a reference of their own per (node, head).
+// scales folded in, on a reference of their own per (node, head): softmax_q8.cuh.
 #include <math.h>
 
 #include <type_traits>
@@ -54,6 +54,7 @@
 #include "mla_device.cuh"
 #include "mla_internal.h"
 #include "sm100.cuh"
+#include "softmax_q8.cuh"
 
 namespace mla {
 namespace {
@@ -73,11 +74,6 @@ constexpr int kProducers = 2;             // warps 0, 1: TMA producers
 constexpr int kWarpMma = kProducers, kWarpSoft0 = kWarpMma + 1, kSoftWarps = 8;
 constexpr int kThreads = 32 * (kWarpSoft0 + kSoftWarps);
 constexpr float kRescaleLog2 = 8.0f;      // lazy rescale threshold (log2 units)
-constexpr float kPLog8 = 4.0f;            // 8-bit MMAs: a weight at the reference is carried as 2^4,
-constexpr float kRescaleLog2Q8 = 4.8f;    // the reference is raised past 4.8 (at most 2^8.8 < 448) ...
-constexpr float kLowerLog2Q8 = 8.0f;      // ... and lowered to a tile whose largest is more than 8 below it, ...
-constexpr float kLowestLog2Q8 = 32.0f;    // ... to 32 below the largest so far at most
-constexpr float kLeastScale8 = 0x1p-48f;  // smaller row scales count as this one (see the softmax)
 // What cutting row tiles costs a call whose pairs are all busy, in tiles of a
 // pair: a second segment, the partials and their merge.  128 sequences of one
 // row tile of two tiles: 49.6 us cut evenly, 34.5 whole; 60 of sixteen: 93 and
@@ -99,9 +95,9 @@ constexpr int kMaxDealt = 1024;           // sequences whose row tiles can be de
 constexpr int kMPart = kMRedSum + 4 * kHM * 4;          // int [8]: where this pair's part begins (see there)
 constexpr int kMCol = kMPart + 4 * 8;                   // int [96]: tiles of each column
 constexpr int kMRt = kMCol + 4 * kMaxPairs;             // uint16 [1024]: row tiles before each sequence
-constexpr int kMScale = kMRt + 2 * kMaxDealt;           // float [4][4 pages][64 rows]: 8-bit MMAs, see the softmax
+constexpr int kMScale = kMRt + 2 * kMaxDealt;           // 8-bit MMAs: the row scales of the four pages, see softmax_q8.cuh
 constexpr int kMScan = kMScale;                         // int2 [16]: per-warp sums of the schedule's scan, before that
-constexpr int kMiscBytes = kMScale + 4 * 4 * 4 * 64;
+constexpr int kMiscBytes = kMScale + q8::kBytes;
 
 template <bool D8>
 struct TreeLayout {
@@ -748,31 +744,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if constexpr (D8) {
         if (my < seq_rows) slq *= p.q_scale[grow];
       }
-      // D8.  The weight MMAs multiply codes, so a row's weight has to carry
-      // its scale: with y_j = z_j + log2 sc_j (z_j in log2 units) the weight
-      // operand is x_j = 16 * 2^(y_j - m), m a reference for the y's that only
-      // rows this thread's (node, head) sees can move.  The sum of the softmax
-      // takes the same x_j over sc_j, so O / sum is the result with no factor
-      // left.  Measured against the scores alone, with the scales relative to
-      // the largest one of the tile, a row of large scale and no weight, or one
-      // that the mask hides, pushed the others' weights below e4m3's last step.
-      // x_j is carried as e4m3(x) + e5m2(x - e4m3(x)): 2^-8 of itself down to
-      // 2^-6, 2^-14 below, so weights to about 2^-21 of the reference count.  m
-      // follows a tile down as well as up (O and the sum are fp32 and take any
-      // factor), so a long thin tail behind one strong row is carried on its
-      // own reference.  With two e4m3 terms and m only rising, weights under
-      // 2^-14 of the strongest were lost but stayed in the sum: with 0.3 to 0.9 of
-      // the mass on the first of 32768 rows o was off by 0.09 to 3.2 of its norm
-      // (now 3e-4 at most; 4096 to 131072 rows: 7e-4).
-      // A page's scales, their logarithms and reciprocals wait in shared
-      // memory; scales below 2^-48 (rows below 2e-12) count as 2^-48, which
-      // keeps the sum finite.  Both warps of a page write the same values; the
-      // reciprocals, read after the tile's sync, alternate by tile.  Each read
-      // is issued four columns before its values are used (128 x 2-6 drafts x
-      // 128 heads over 2048-4096 rows: 458 us a call without that, 425 with it;
-      // two shuffles per column instead 430).
-      float* page_sc = reinterpret_cast<float*>(misc + kMScale) + part * 64;   // scales, logarithms, 2 x reciprocals
-      constexpr int kScalePlane = 4 * 64;
+      float* page_sc = reinterpret_cast<float*>(misc + kMScale) + part * 64;   // D8: see softmax_q8.cuh
       float m_run = -INFINITY, m_top = -INFINITY, l_acc = 0.f;
       for (int i = 0; i < s.nt; ++i) {
         const uint32_t t = gt + i;
@@ -794,17 +766,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         }
-        float* page_inv = page_sc + (2 + sb) * kScalePlane;
-        if constexpr (D8) {
-          const float a = fmaxf(sc_lo, kLeastScale8), c = fmaxf(sc_hi, kLeastScale8);
-          page_sc[lane] = sc_lo;
-          page_sc[lane + 32] = sc_hi;
-          page_sc[kScalePlane + lane] = log2f(a);
-          page_sc[kScalePlane + lane + 32] = log2f(c);
-          page_inv[lane] = 1.0f / a;
-          page_inv[lane + 32] = 1.0f / c;
-          __syncwarp();
-        }
+        float* page_inv = page_sc + (2 + sb) * q8::kPlane;
+        if constexpr (D8) q8::put_scales(page_sc, page_inv, lane, sc_lo, sc_hi);
         const bool full = __all_sync(0xffffffffu, vis == ~0ull);
         ok = __all_sync(0xffffffffu, mbar_wait<false>(bar(kBSFull + sb), (t >> 1) & 1, abort_flag, lim));
         if (!ok) break;
@@ -816,20 +779,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         float mx = -INFINITY;
         if constexpr (D8) {
-          const uint32_t a_sc = smem_u32(page_sc);
-          float4 sc_n = ld_shared_f4(a_sc), lg_n = ld_shared_f4(a_sc + 4 * kScalePlane);
-#pragma unroll
-          for (int j = 0; j < 64; j += 4) {
-            const float4 sc = sc_n, lg = lg_n;
-            if (j < 60) {
-              sc_n = ld_shared_f4(a_sc + 4 * (j + 4));
-              lg_n = ld_shared_f4(a_sc + 4 * (kScalePlane + j + 4));
-            }
-            v[j] = fmaf(v[j] * slq, sc.x, lg.x);
-            v[j + 1] = fmaf(v[j + 1] * slq, sc.y, lg.y);
-            v[j + 2] = fmaf(v[j + 2] * slq, sc.z, lg.z);
-            v[j + 3] = fmaf(v[j + 3] * slq, sc.w, lg.w);
-          }
+          q8::scores(v, slq, page_sc);
         } else {
 #pragma unroll
           for (int j = 0; j < 64; ++j) v[j] *= slq;
@@ -849,38 +799,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         rm[part * kHM + hh] = mx;
         if (!(ok = soft_sync())) break;
         const float tmax = fmaxf(fmaxf(rm[hh], rm[kHM + hh]), fmaxf(rm[2 * kHM + hh], rm[3 * kHM + hh]));
-        float m_new = (tmax > m_run + (D8 ? kRescaleLog2Q8 : kRescaleLog2)) ? tmax : m_run;
-        if constexpr (D8) {
-          m_top = fmaxf(m_top, tmax);
-          if (tmax < m_run - kLowerLog2Q8 && tmax > -INFINITY) m_new = fmaxf(tmax, m_top - kLowestLog2Q8);
-        }
+        float m_new;
+        if constexpr (D8) m_new = q8::reference(m_run, tmax, m_top);
+        else m_new = tmax > m_run + kRescaleLog2 ? tmax : m_run;
         const bool changed = m_new != m_run;
         // factor for the sums and the accumulator kept so far (0 when nothing was kept)
         const float alpha = (m_run == -INFINITY) ? 0.f : exp2_approx(m_run - m_new);
         m_run = m_new;
-        const float msub = m_new == -INFINITY ? 0.f : (D8 ? m_new - kPLog8 : m_new);
         uint32_t pk[32];   // D8: pk[0..15] the hi codes of the 64 rows, pk[16..31] the lo codes
         float sum = 0.f;
         if constexpr (D8) {
-          float sum2 = 0.f;
-          const uint32_t a_inv = smem_u32(page_inv);
-          float4 inv_n = ld_shared_f4(a_inv);
-#pragma unroll
-          for (int j = 0; j < 64; j += 4) {
-            const float4 inv = inv_n;
-            if (j < 60) inv_n = ld_shared_f4(a_inv + 4 * (j + 4));
-            const float x0 = exp2_approx(v[j] - msub), x1 = exp2_approx(v[j + 1] - msub);
-            const float x2 = exp2_approx(v[j + 2] - msub), x3 = exp2_approx(v[j + 3] - msub);
-            sum = fmaf(x1, inv.y, fmaf(x0, inv.x, sum));
-            sum2 = fmaf(x3, inv.w, fmaf(x2, inv.z, sum2));
-            uint32_t h01, l01, h23, l23;
-            split_e4m3_e5m2x2(x0, x1, h01, l01);
-            split_e4m3_e5m2x2(x2, x3, h23, l23);
-            pk[j >> 2] = h01 | h23 << 16;
-            pk[16 + (j >> 2)] = l01 | l23 << 16;
-          }
-          sum += sum2;
+          sum = q8::weights(v, m_new, page_inv, pk);
         } else {
+          const float msub = m_new == -INFINITY ? 0.f : m_new;
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             const float p0 = exp2_approx(v[2 * j] - msub), p1 = exp2_approx(v[2 * j + 1] - msub);
@@ -948,7 +879,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // a first segment that continues a row tile: slot 2 pair; a last one that leaves its row tile open: 2 pair + 1
         const int slot = 2 * pair + (s.k0 == 0 ? 1 : 0);
         if (part == 0) {
-          const float lv = lt > 0.f ? (m_run - (D8 ? kPLog8 : 0.f) + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+          const float lv = lt > 0.f ? (m_run - (D8 ? q8::kLog : 0.f) + log2f(lt)) * 0.69314718055994531f : -INFINITY;
           if (!whole) p.part_lse[slot * kM + kHM * (int)rank + hh] = lv;
           else if (p.lse && my < seq_rows) p.lse[grow] = lv;
         }
