@@ -367,7 +367,9 @@ mla_status mla_cache_append_slots(const void* kv_a, mla_dtype kv_dtype, int n_ne
  * Bytes of caller workspace mla_decode_tree needs for a call of max_rows rows
  * with this cache: for bf16 a fixed 50 MB of fp32 partials, for e4m3 also
  * 1156 bytes per (row, head) for the two-term query, for fp32 2052 bytes per
- * (row, head) and split (the fewer rows, the more splits, at most 64).
+ * partial (at most 64 per (row, head), and at most 9472 more than there are
+ * (row, head) pairs).  Never less for more rows or heads: a workspace for a
+ * model's largest step serves its smaller ones.
  * 0 for non-positive sizes or an unknown dtype.
  */
 size_t mla_decode_tree_workspace_bytes(mla_dtype cache_dtype, int max_rows, int n_heads);

@@ -1365,10 +1365,21 @@ __global__ void __launch_bounds__(512) tree_merge_f32_kernel(TreeParams p, int s
 
 // ------------------------------------------------------------------ host side
 // Splits of the fp32 form: enough CTAs for four per SM of a B200, at most 64.
+constexpr int kSimtCtas = 4 * 148, kSimtSplits = 64;
 int splits_f32(long long rows, int n_heads) {
   const long long ctas = rows * ((n_heads + kSimtHeads - 1) / kSimtHeads);
-  const long long want = (4 * 148 + ctas - 1) / ctas;
-  return (int)(want < 64 ? want : 64);
+  const long long want = (kSimtCtas + ctas - 1) / ctas;
+  return (int)(want < kSimtSplits ? want : kSimtSplits);
+}
+
+// Partials that a call of `vec` (row, head) pairs may leave: at most kSimtSplits
+// per pair, and since splits < kSimtCtas / ctas + 1 and a CTA takes up to
+// kSimtHeads pairs, fewer than vec + kSimtHeads * kSimtCtas.  The bound grows
+// with vec (vec * splits itself falls where splits drops by one), so that a
+// workspace for a larger call holds a smaller one.
+size_t partials_f32(size_t vec) {
+  const size_t by_splits = vec * kSimtSplits, by_ctas = vec + (size_t)kSimtHeads * kSimtCtas;
+  return by_splits < by_ctas ? by_splits : by_ctas;
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -1381,9 +1392,9 @@ TreeWorkspace tree_workspace(int cache_dtype, long long rows, int n_heads) {
   TreeWorkspace w{};
   const size_t vec = (size_t)rows * n_heads;
   if (cache_dtype == MLA_F32) {
-    const size_t splits = (size_t)splits_f32(rows, n_heads);
-    w.lse = up256(vec * splits * MLA_D_C * sizeof(float));
-    w.bytes = w.lse + up256(vec * splits * sizeof(float));
+    const size_t parts = partials_f32(vec);
+    w.lse = up256(parts * MLA_D_C * sizeof(float));
+    w.bytes = w.lse + up256(parts * sizeof(float));
     return w;
   }
   w.lse = (size_t)2 * kMaxPairs * kM * MLA_D_C * sizeof(float);
