@@ -99,9 +99,14 @@ struct Reader {
     Reader r{args};                                                                                   \
     __VA_ARGS__                                                                                       \
   }
+// (other threads run meanwhile: a launch may wait for room in the stream's queue)
 #define MLA_CALL(expr)        \
   if (!r.ok) return nullptr;  \
-  return PyLong_FromLong(static_cast<long>(expr));
+  mla_status status;          \
+  Py_BEGIN_ALLOW_THREADS      \
+  status = (expr);            \
+  Py_END_ALLOW_THREADS        \
+  return PyLong_FromLong(static_cast<long>(status));
 
 MLA_ENTRY(step_plan, 23, {
   auto* lens = r.as<const int32_t>(); auto* counts = r.as<const int32_t>(); auto* parents = r.as<const int32_t>();
