@@ -86,6 +86,8 @@ class StepPlan:
         if stream is None:
             self.seq_lens.copy_(self.kv_lens)
             return
+        if isinstance(stream, int):
+            stream = self.torch.cuda.ExternalStream(stream, device=self.device)
         with self.torch.cuda.stream(stream):
             self.seq_lens.copy_(self.kv_lens)
 
