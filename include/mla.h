@@ -334,8 +334,9 @@ mla_status mla_decode_fwd_q8(const void* q8, const float* q_scale, const void* c
  *               that the calls that follow do no work.  MLA_DEVERR_PAGE: a row's page
  *               is outside the pool; its slot is -1.
  * Except held and free_count, outputs must not overlap inputs.  Host limits:
- * num_pages * page_size, max_pages_per_seq * page_size and batch *
- * max_pages_per_seq below 2^31.  One launch up to 4096 rows, two above.
+ * num_pages * page_size, max_pages_per_seq * page_size, batch *
+ * max_pages_per_seq and max_rows + 4096 below 2^31, mask_words below 2^25.  One
+ * launch up to 4096 rows and 1024 sequences, two above.
  */
 mla_status mla_step_plan(const int32_t* seq_lens, const int32_t* new_counts, const int32_t* parents, int batch,
                          int max_rows, int mask_words, const int32_t* held_in, int32_t* held_out, int32_t* free_pages,

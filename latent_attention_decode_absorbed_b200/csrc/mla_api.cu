@@ -228,6 +228,9 @@ mla_status mla_step_plan(const int32_t* seq_lens, const int32_t* new_counts, con
   MLA_REQUIRE((long long)max_pages_per_seq * page_size < (1ll << 31) && (long long)num_pages * page_size < (1ll << 31) &&
                   (long long)batch * max_pages_per_seq < (1ll << 31),
               MLA_ERR_UNSUPPORTED, "mla_step_plan: table or pool beyond int32 slots");
+  // a row index plus a thread's stride, and a tree's 64 mask_words nodes, are ints
+  MLA_REQUIRE((long long)max_rows + 4096 < (1ll << 31) && mask_words < (1 << 25), MLA_ERR_UNSUPPORTED,
+              "mla_step_plan: max_rows or mask_words too large");
   MLA_REQUIRE(seq_lens && new_counts && held_in && held_out && free_pages && free_count_in && free_count_out &&
                   block_table && row_start && kv_lens && (max_rows == 0 || (positions && slots)),
               MLA_ERR_INVALID_ARG, "mla_step_plan: null pointer");
