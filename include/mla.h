@@ -444,8 +444,9 @@ mla_status mla_decode_tree(const void* q_abs, mla_dtype q_dtype, const void* cac
  *                 and needs the lengths once), not one of the inputs
  *   err_word      device int32 or NULL.  MLA_DEVERR_POSITION: impossible numbers or a
  *                 path that does not ascend within the tree; the sequence keeps its
- *                 rows and seq_lens_out[b] = P_b.  MLA_DEVERR_PAGE: a row's page is
- *                 outside the pool; that row is not moved.
+ *                 rows and seq_lens_out[b] = P_b (0 where kv_lens and row_start give
+ *                 none).  MLA_DEVERR_PAGE: a row's page is outside the pool; that row
+ *                 is not moved.
  */
 mla_status mla_cache_commit(const int32_t* kv_lens, const int32_t* row_start, int batch, int max_rows,
                             const int32_t* accept_counts, const int32_t* accept_nodes, const int32_t* block_table,

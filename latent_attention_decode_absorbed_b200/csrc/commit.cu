@@ -26,17 +26,18 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(CommitArgs a) {
   griddep_wait();
   griddep_launch_dependents();
   const int b = blockIdx.x, part = blockIdx.y, tid = threadIdx.x;
-  const int start = a.row_start[b], n = a.row_start[b + 1] - start;
-  const int base = a.kv_lens[b] - n;            // the prefix
-  const int count = a.counts[b];
+  const int start = a.row_start[b], end = a.row_start[b + 1], kv = a.kv_lens[b], count = a.counts[b];
+  // differences only of numbers that are known not to wrap
+  bool bad = start < 0 || end < start || end > a.n_rows || kv < end - start;
+  const int n = bad ? 0 : end - start;
+  const int base = bad ? 0 : kv - n;            // the prefix
+  bad |= kv > a.max_pages * 64 || count < 0 || count > n;
   const int32_t* path = a.nodes + start;
-  bool bad = start < 0 || n < 0 || base < 0 || a.kv_lens[b] > a.max_pages * 64 || count < 0 || count > n ||
-             start > a.n_rows - n;
   if (!bad)
     for (int j = tid; j < count; j += kThreads) bad |= path[j] < 0 || path[j] >= n || (j && path[j] <= path[j - 1]);
   bad = __syncthreads_or(bad);
   if (bad && tid == 0 && part == 0) flag_error(a.err, MLA_DEVERR_POSITION);
-  if (tid == 0 && part == 0 && a.seq_lens) a.seq_lens[b] = bad ? max(base, 0) : base + count;
+  if (tid == 0 && part == 0 && a.seq_lens) a.seq_lens[b] = bad ? base : base + count;
   if (bad) return;
   const int32_t* table = a.block_table + (size_t)b * a.max_pages;
   // slot of a cached row, -1 for a page outside the pool
