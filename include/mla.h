@@ -386,8 +386,9 @@ size_t mla_decode_tree_workspace_bytes(mla_dtype cache_dtype, int max_rows, int 
  * row L_b - n_b + k) whose bit is set in its mask.  Over those rows
  *   z_j = softmax_scale * (q_abs[r,h,0:512] . c_j + q_abs[r,h,512:576] . k_j)
  *   o_lat[r,h,:] = sum_j e^{z_j - m} c_j / sum_j e^{z_j - m},  lse_out[r,h] = m + ln sum_j e^{z_j - m}
- * A row that sees nothing gets o_lat = 0 and lse_out = -inf.  One row per
- * sequence (no drafts) is the single-token decode.
+ * A row that sees nothing gets o_lat = 0 and lse_out = -inf, a (row, head) with a
+ * NaN score NaN in both.  One row per sequence (no drafts) is the single-token
+ * decode.
  *   q_abs       device [max_rows, n_heads, 576], q_dtype F32 or BF16
  *   cache, cache_scale, block_table  as for mla_decode_fwd (its pool contract too:
  *               rows of a visited page behind the sequence's end and drafted rows

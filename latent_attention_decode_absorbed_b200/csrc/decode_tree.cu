@@ -874,12 +874,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (ok) {
         const float lt = red_sum[hh] + red_sum[kHM + hh] + red_sum[2 * kHM + hh] + red_sum[3 * kHM + hh];
-        const float inv_l = lt > 0.f ? 1.f / lt : 0.f;
+        const float inv_l = lt == 0.f ? 0.f : 1.f / lt;        // (a NaN sum, of NaN scores, stays one)
         const bool whole = s.nt == s.kt;
         // a first segment that continues a row tile: slot 2 pair; a last one that leaves its row tile open: 2 pair + 1
         const int slot = 2 * pair + (s.k0 == 0 ? 1 : 0);
         if (part == 0) {
-          const float lv = lt > 0.f ? (m_run - (D8 ? q8::kLog : 0.f) + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+          const float lv = lt == 0.f ? -INFINITY : (m_run - (D8 ? q8::kLog : 0.f) + log2f(lt)) * 0.69314718055994531f;
           if (!whole) p.part_lse[slot * kM + kHM * (int)rank + hh] = lv;
           else if (p.lse && my < seq_rows) p.lse[grow] = lv;
         }
@@ -1049,7 +1049,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const floa
     float top = mx;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) top = fmaxf(top, w[k]);
-    if (top == -INFINITY) continue;          // nothing seen so far
+    if (top == -INFINITY) {                  // nothing seen so far, unless a NaN that the maximum passed over
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (isnan(w[k])) sum = w[k];
+      continue;
+    }
     const float old = expf(mx - top);
     mx = top;
     sum *= old;
@@ -1069,12 +1074,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const floa
     }
   }
   if (row >= d.rows) return;
-  const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
   const size_t out = (size_t)d.row0 + row;
   const int dim = 256 * ch + 128 * (q4 >> 1) + 4 * q;
 #pragma unroll
   for (int i = 0; i < 2; ++i) store4(o_lat + out * MLA_D_C + dim + 4 * i, acc[i], inv);
-  if (lse_out && dim == 0) lse_out[out] = sum > 0.f ? mx + logf(sum) : -INFINITY;
+  if (lse_out && dim == 0) lse_out[out] = sum == 0.f ? -INFINITY : mx + logf(sum);
 }
 
 // The two-term e4m3 query of the 8-bit form: per (node, head) vector
@@ -1309,10 +1314,10 @@ __global__ void __launch_bounds__(32 * kSimtWarps, 2) decode_tree_simt_kernel(co
   for (int e = 0; e < kSimtPer; ++e) {
     if (e >= heads) break;
     const size_t base = (vec + e) * splits + split;
-    const float inv = l[e] > 0.f ? 1.0f / l[e] : 0.f;
+    const float inv = l[e] == 0.f ? 0.f : 1.0f / l[e];
 #pragma unroll
     for (int k = 0; k < 16; ++k) p.part_o[base * MLA_D_C + lane + 32 * k] = o[e][k] * inv;
-    if (lane == 0) p.part_lse[base] = l[e] > 0.f ? m[e] + logf(l[e]) : -INFINITY;
+    if (lane == 0) p.part_lse[base] = l[e] == 0.f ? -INFINITY : m[e] + logf(l[e]);
   }
 }
 
@@ -1336,8 +1341,9 @@ __global__ void __launch_bounds__(512) tree_merge_f32_kernel(TreeParams p, int s
   SeqInfo s;
   const bool valid = seq_of(p, (int)(vec / p.n_heads), s) >= 0;
   const float mx = warp_max(fmaxf(l0, l1));
-  l0 = mx == -INFINITY ? 0.f : expf(l0 - mx);
-  l1 = mx == -INFINITY ? 0.f : expf(l1 - mx);
+  const float ref = mx == -INFINITY ? 0.f : mx;          // nothing seen: weights e^-inf (a NaN stays one)
+  l0 = expf(l0 - ref);
+  l1 = expf(l1 - ref);
   const float sum = warp_sum(l0 + l1);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -1359,8 +1365,8 @@ __global__ void __launch_bounds__(512) tree_merge_f32_kernel(TreeParams p, int s
     acc.z += x.z;
     acc.w += x.w;
   }
-  store4(reinterpret_cast<OT*>(p.o_lat) + vec * MLA_D_C + 4 * c, acc, sum > 0.f ? 1.0f / sum : 0.f);
-  if (p.lse && c == 0) p.lse[vec] = sum > 0.f ? mx + logf(sum) : -INFINITY;
+  store4(reinterpret_cast<OT*>(p.o_lat) + vec * MLA_D_C + 4 * c, acc, sum == 0.f ? 0.f : 1.0f / sum);
+  if (p.lse && c == 0) p.lse[vec] = sum == 0.f ? -INFINITY : mx + logf(sum);
 }
 
 // ------------------------------------------------------------------ host side
