@@ -24,7 +24,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmla.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
-BINDING = os.path.join(PKG, "_native.so")     # the Python module that marshals the drafted-step calls
+# the Python module that marshals the drafted-step calls, named for the interpreter it is built for: another one
+# does not see it and builds its own
+BINDING = os.path.join(PKG, "_native" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -82,6 +84,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
 
 def _build_binding(force: bool, verbose: bool):
     """The Python module over libmla.so (found next to it at load time)."""
+    untagged = os.path.join(PKG, "_native.so")        # an older build's, which any interpreter would load
+    if os.path.exists(untagged):
+        os.remove(untagged)
     newest = max(os.path.getmtime(f) for f in [BINDING_SRC, os.path.join(INCLUDE, "mla.h")])
     if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
         return
