@@ -24,17 +24,32 @@ import math
 
 import numpy as np
 
-from . import (D_C, D_R, D_ROW, D_V, MLA_DEVERR_CAPACITY, MLA_E4M3, MLA_F32, PAGE, mla_absorb_q, mla_cache_append_slots,
-               mla_cache_commit, mla_decode_tree, mla_decode_tree_workspace_bytes, mla_out_uv, mla_rope_table,
-               mla_step_plan)
+from . import (D_C, D_NOPE, D_R, D_ROW, D_V, MLA_DEVERR_CAPACITY, MLA_E4M3, MLA_F32, PAGE, mla_absorb_q,
+               mla_cache_append_slots, mla_cache_commit, mla_decode_tree, mla_decode_tree_workspace_bytes, mla_out_uv,
+               mla_rope_table, mla_step_plan)
 from .step import _DT, _torch_dtype
+
+
+def _need(name, t, cuda, dtype, n):
+    """Raise unless a kernel (on the GPU: cuda) can read n numbers of t: the calls take its address and the plan's
+    sizes, nothing else.  (Integer addresses pass, as in the calls.  A layer makes five of these, 0.4 us each.)"""
+    if isinstance(t, int) or (t.dtype is dtype and t.is_cuda is cuda and t.numel() >= n and t.is_contiguous()):
+        return
+    if t.dtype is not dtype or t.numel() < n:
+        raise ValueError(f"{name}: need {n} numbers of {dtype}, got {t.dtype} {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if not t.is_pinned():
+        raise ValueError(f"{name} is on {t.device}, the plan is not")
 
 
 class StepPlan:
     """The bookkeeping of `batch` sequences over a pool of `num_pages` pages.
 
     max_pages: pages a sequence may hold; max_rows: new rows of one step, all
-    sequences together; max_nodes: rows of one sequence's drafted tree."""
+    sequences together; max_nodes: rows of one sequence's drafted tree, and of
+    every other sequence's in a step with trees (a longer prompt waits for a
+    step without)."""
 
     def __init__(self, *, batch, num_pages, max_pages, max_rows, max_nodes=64, device="cuda"):
         import torch
@@ -42,6 +57,7 @@ class StepPlan:
         self.batch, self.num_pages, self.max_pages = int(batch), int(num_pages), int(max_pages)
         self.max_rows, self.mask_words = int(max_rows), -(-int(max_nodes) // 64)
         self.device = torch.device(device)
+        self.cuda = self.device.type == "cuda"
 
         def ints(*shape, fill=0):
             return torch.full(shape, fill, dtype=torch.int32, device=self.device)
@@ -63,6 +79,9 @@ class StepPlan:
         """Lay out a step: int32 new_counts [batch] rows per sequence; parents
         int32 [max_rows] (each row's parent within its sequence's rows, -1 for
         a root) for drafted trees, or None for runs of tokens."""
+        _need("new_counts", new_counts, self.cuda, self.torch.int32, self.batch)
+        if parents is not None:
+            _need("parents", parents, self.cuda, self.torch.int32, self.max_rows)
         self.is_tree = parents is not None
         mla_step_plan(self.seq_lens, new_counts, parents, self.batch, self.max_rows, self.mask_words, self.held,
                       self.held, self.free_pages, self.free_count, self.free_count, self.block_table, self.max_pages,
@@ -75,6 +94,8 @@ class StepPlan:
         seq_lens then counts them."""
         if not layers:
             raise ValueError("commit needs the layers whose caches hold the step's rows")
+        _need("accept_counts", accept_counts, self.cuda, self.torch.int32, self.batch)
+        _need("accept_nodes", accept_nodes, self.cuda, self.torch.int32, self.max_rows)
         for i, layer in enumerate(layers):
             last = i == len(layers) - 1
             mla_cache_commit(self.kv_lens, self.row_start, self.batch, self.max_rows, accept_counts, accept_nodes,
@@ -141,12 +162,19 @@ class TreeDecodeStep:
         """Cache rows of the planned tokens: kv_a [max_rows, 576] (rows behind the
         step's last one are skipped)."""
         p = self.plan
-        mla_cache_append_slots(kv_a, MLA_F32 if kv_a.dtype == p.torch.float32 else _DT["bf16"], p.max_rows, p.slots,
+        f32 = kv_a.dtype is p.torch.float32
+        _need("kv_a", kv_a, p.cuda, kv_a.dtype if f32 else p.torch.bfloat16, p.max_rows * D_ROW)
+        mla_cache_append_slots(kv_a, MLA_F32 if f32 else _DT["bf16"], p.max_rows, p.slots,
                                p.positions, self.norm_gain, self.eps, self.rope_cos, self.rope_sin, self.max_pos,
                                self.cache, self.cache_scale, self.cache_dtype, p.num_pages, p.err, stream)
 
     def absorb(self, q_nope, q_pe, w_uk, stream=None):
-        """q_abs = [W_UK^T q_nope; q_pe]; q_pe rotated to the rows' `plan.positions`."""
+        """q_abs = [W_UK^T q_nope; q_pe], q_nope [max_rows, H, 128], q_pe [max_rows, H, 64] rotated to the rows'
+        `plan.positions`, w_uk [H, 128, 512], all of `dtype`."""
+        cuda, dt, vecs = self.plan.cuda, self.q_abs.dtype, self.plan.max_rows * self.n_heads
+        _need("q_nope", q_nope, cuda, dt, vecs * D_NOPE)
+        _need("q_pe", q_pe, cuda, dt, vecs * D_R)
+        _need("w_uk", w_uk, cuda, dt, self.n_heads * D_NOPE * D_C)
         mla_absorb_q(q_nope, q_pe, w_uk, self.q_abs, self.plan.max_rows, self.n_heads, self.dtype, stream)
 
     def attend(self, stream=None):
@@ -157,6 +185,8 @@ class TreeDecodeStep:
                         self.o_lat, self.dtype, self.lse, p.err, stream)
 
     def project_out(self, w_uv, stream=None):
+        """`out` = W_UV o_lat; w_uv [H, 128, 512] of `dtype`."""
+        _need("w_uv", w_uv, self.plan.cuda, self.o_lat.dtype, self.n_heads * D_V * D_C)
         mla_out_uv(self.o_lat, w_uv, self.out, self.plan.max_rows, self.n_heads, self.dtype, stream)
 
     def run(self, kv_a, q_nope, q_pe, w_uk, w_uv, stream=None):
