@@ -712,7 +712,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // ================= softmax (both CTAs, warps 2-9) =================
+    // ================= softmax (both CTAs, warps 3-10) =================
     // Thread (lane quadrant q4, column half ch, lane) owns row hh = 32 (q4 & 1)
     // + lane of this CTA and the 64 tile rows 128 (q4 >> 1) + 64 ch .. +63.
     const int q4 = warp & 3;
