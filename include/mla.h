@@ -276,9 +276,9 @@ mla_status mla_split_q_e4m3(const void* q_abs, int rows, int n_heads, void* q8, 
  * GEMM of (hi + lo) with row j's codes.  The value GEMM's weights are x_j =
  * 16 * 2^(log2 e * z_j + log2 cache_scale[j] - m), m a running reference per query
  * row and head (raised once a tile's largest exceeds it by 4.8, lowered once it
- * is more than 8 below), carried as e4m3(x) + e5m2(x - e4m3(x)): to 2^-8 of
- * themselves or 2^-18 of the reference.  Row scales below 2^-48 count as 2^-48
- * there.  o_part then holds
+ * is more than 8 below, to 32 below the largest so far at most), carried as
+ * e4m3(x) + e5m2(x - e4m3(x)): to 2^-8 of themselves or 2^-18 of the reference.
+ * Row scales below 2^-48 count as 2^-48 there.  o_part then holds
  *   sum_j e^{z_j - m} (codes_j * cache_scale[j])[0:512] / sum_j e^{z_j - m}
  * to within that error per weight.
  *   q8, q_scale  from mla_split_q_e4m3 for batch*q_len rows and n_heads
@@ -414,8 +414,8 @@ size_t mla_decode_tree_workspace_bytes(mla_dtype cache_dtype, int max_rows, int 
  * enter the value product as bf16 (BF16 cache) or, times their row's scale, as an
  * e4m3 and an e5m2 term (E4M3 cache, whose queries must be finite): to 2^-8 of
  * themselves or 2^-18 of a reference that is at most 2^8 times the largest weight
- * among the same 256 rows; row scales below 2^-48 count as 2^-48.  Scores, sums
- * and statistics are fp32.
+ * among the same 256 rows (or 2^-32 of the largest among earlier ones); row scales
+ * below 2^-48 count as 2^-48.  Scores, sums and statistics are fp32.
  * Results do not depend on timing: a call on the same inputs and GPU returns
  * the same bits.  Calls that share a workspace must not overlap on the GPU, so
  * two captured graphs that may replay at once need a workspace each.
